@@ -303,6 +303,100 @@ sq_status sq_w8a8_gemm_fp8(const uint8_t* xq, const float* sx, const uint8_t* wq
                            int64_t M, int64_t N, int64_t K, void* y, sq_dtype ydt, int64_t ldy,
                            void* workspace, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Weight-only 4-bit variant.  "量化：只压权重，与训练后量化（PTQ）" (decode roofline: group-128 INT4
+ * weights with 16-bit activations read a quarter of BF16's bytes; AWQ paragraph: Q(W diag(s))
+ * with the same smoothing) next to W8A8: at a few tokens a linear layer is bound by its weights'
+ * bytes.  The pages fix no storage format; the library's is:
+ *   - Codes are 4 bits, 0 .. 15.  The row of an output channel is its K codes in blocks of 128,
+ *     64 bytes per block, sq_w4_row_bytes(K) = 64 ceil(K / 128) bytes in all; a last, short block
+ *     is padded with zero nibbles.  The code of k = 128 b + 32 w + 8 t + i (w, t < 4, i < 8) is
+ *     nibble i / 2 + 4 (i % 2) (counted from the low end) of the little-endian 32-bit word at byte
+ *     64 b + 16 t + 4 w of the row.
+ *   - A group is `group` (32, 64 or 128) consecutive input channels of one output channel; the
+ *     last one may be short.  scales: bf16 (bit patterns), [ceil(K / group), N]; zeros: uint8
+ *     0 .. 15 of the same shape, or NULL, which means 8 everywhere (symmetric).
+ *   - A code stands for (code - zero) * scale.  Scales are bf16 because they are read with the
+ *     codes (2 bytes per group instead of 4); codes are taken against the rounded scale, so the
+ *     rounding does not add to the quantisation error.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Bytes of one packed row of K codes (-1 for K < 0). */
+int64_t sq_w4_row_bytes(int64_t K);
+
+/* sq_fold_quant_weights_w4 -- sq_fold_quant_weights with 4-bit group-wise weights:
+ *   W'[j, n] = s_j * W[j, n]   (s may be NULL: W' = W)
+ *   zeros == NULL: scale = bf16(max|W'| / 7), code = 8 + clamp(rne(W' / scale), -7, 7)
+ *   zeros != NULL: lo = min(0, min W'), hi = max(0, max W'), scale = bf16((hi - lo) / 15),
+ *                  zero = clamp(rne(-lo / scale), 0, 15), code = clamp(rne(W' / scale) + zero, 0, 15)
+ *   over the group's channels j; a zero scale gives the code 8 (zeros == NULL) or zero point and
+ *   code 0.  Wq: [N, sq_w4_row_bytes(K)] bytes, 16-byte aligned.  W must be finite.  K % 16 == 0,
+ *   K <= SQ_MAX_K.  gamma_f, beta_f as for sq_fold_quant_weights (with s NULL: copies). */
+sq_status sq_fold_quant_weights_w4(const void* W, sq_dtype dt, int64_t K, int64_t N, int64_t ldw, const float* s,
+                                   const float* gamma, const float* beta, int group, uint8_t* Wq, uint16_t* scales,
+                                   uint8_t* zeros, float* gamma_f, float* beta_f, void* stream);
+
+/* sq_w4_dequant -- the values that packed weights stand for:
+ *   y[n, k] = (code[n, k] - zero) * scale, exact in binary32, rounded once for SQ_BF16.
+ *   y: [N, K] with leading dimension ldy >= K, 16-byte aligned rows.  K % 16 == 0. */
+sq_status sq_w4_dequant(const uint8_t* Wq, const uint16_t* scales, const uint8_t* zeros, int64_t K, int64_t N,
+                        int group, void* y, sq_dtype ydt, int64_t ldy, void* stream);
+
+/* Most tokens of one sq_w4_gemm call. */
+#define SQ_W4_MAX_M 65536
+
+/* sq_w4_gemm -- the product with packed weights, for a few tokens (decode):
+ *   y[m, n] = sum over groups of scale * (sum over the group's k of (code[n, k] - zero) * x[m, k])
+ *   x: [M, K] bf16 or fp32, ldx; both enter exactly (fp32 as a sum of three bf16 numbers), sums are
+ *   binary32, and the result is rounded once to ydt (SQ_BF16 or SQ_F32).  y: [M, N], ldy >= N,
+ *   aligned to its element size.  K % 16 == 0, K <= SQ_MAX_K.  Weights are read once for up to 32
+ *   tokens; more tokens (up to SQ_W4_MAX_M) read them again, from L2 where they fit.  No workspace;
+ *   the order of the sums depends on the sizes alone, so equal calls give equal bits. */
+sq_status sq_w4_gemm(const void* x, sq_dtype dt, int64_t M, int64_t K, int64_t ldx, const uint8_t* Wq,
+                     const uint16_t* scales, const uint8_t* zeros, int64_t N, int group, void* y, sq_dtype ydt,
+                     int64_t ldy, void* stream);
+
+/* Limits of sq_moe_w4. */
+#define SQ_MOE_MAX_TOKENS 64
+#define SQ_MOE_MAX_EXPERTS 1024
+#define SQ_MOE_MAX_TOP_K 32
+
+/* sq_moe_w4 -- a whole mixture-of-experts layer for a few tokens, experts packed in 4 bits:
+ *   logits[t, e] = sum_d x[t, d] * Wr[e, d]   (binary64 sums)
+ *   p = softmax over the E experts; ids[t, :] = the top_k largest, largest first, ties to the
+ *   lowest index (a NaN logit ranks last); weights[t, :] = their p, divided by their sum if renorm
+ *   h = silu(W1_e x_t) * (W3_e x_t), silu(v) = v / (1 + exp(-v))
+ *   y[t] = sum over the chosen e of weight * (W2_e h)
+ *   Sums are binary32 (16 significant bits of h enter the last product; 24 where x is SQ_F32) and
+ *   y is rounded once to ydt.
+ *   x: [T, D] bf16/fp32, ldx, 16-byte aligned rows; Wr: [E, D] dense bf16/fp32 (rdt), 16-byte aligned.
+ *   W13: [E, 2 F, sq_w4_row_bytes(D)] packed, the F rows of W1 (gate) first, then the F rows of W3
+ *   (up); s13: bf16 [E, ceil(D / group), 2 F].  W2: [E, D, sq_w4_row_bytes(F)]; s2:
+ *   [E, ceil(F / group), D].  z13, z2: zero points shaped like the scales, both or neither.
+ *   ids: int32 [T, top_k], weights: fp32 [T, top_k], written.  y: [T, D], ldy >= D.
+ *   D % 16 == 0, F % 16 == 0, both <= SQ_MAX_K; T <= SQ_MOE_MAX_TOKENS (more: SQ_ERR_UNSUPPORTED).
+ *   workspace: sq_moe_w4_workspace_size(T, D, F, E, top_k) bytes, 256-byte aligned, zero-filled
+ *   once before its first use; every call leaves it ready for the next, whatever its sizes.  Calls
+ *   that share one must be ordered (on one stream, or by events). */
+sq_status sq_moe_w4(const void* x, sq_dtype dt, int64_t T, int64_t D, int64_t ldx, const void* Wr, sq_dtype rdt,
+                    int64_t E, int top_k, int renorm, int32_t* ids, float* weights, const uint8_t* W13,
+                    const uint16_t* s13, const uint8_t* z13, const uint8_t* W2, const uint16_t* s2, const uint8_t* z2,
+                    int64_t F, int group, void* y, sq_dtype ydt, int64_t ldy, void* workspace, size_t ws_bytes,
+                    void* stream);
+
+/* sq_moe_w4_routed -- the experts of sq_moe_w4 for choices made elsewhere: ids int32 [T, top_k] and
+ * weights fp32 [T, top_k] are read.  An id outside [0, E) is left out (a masked choice; a token
+ * with none left gets a zero row); an expert that a token names more than once counts once, with
+ * the sum of the weights. */
+sq_status sq_moe_w4_routed(const void* x, sq_dtype dt, int64_t T, int64_t D, int64_t ldx, const int32_t* ids,
+                           const float* weights, int64_t E, int top_k, const uint8_t* W13, const uint16_t* s13,
+                           const uint8_t* z13, const uint8_t* W2, const uint16_t* s2, const uint8_t* z2, int64_t F,
+                           int group, void* y, sq_dtype ydt, int64_t ldy, void* workspace, size_t ws_bytes,
+                           void* stream);
+
+/* Workspace bytes of sq_moe_w4 and sq_moe_w4_routed ((size_t)-1 for sizes outside the limits). */
+size_t sq_moe_w4_workspace_size(int64_t T, int64_t D, int64_t F, int64_t E, int top_k);
+
 /* Reads (and with clear != 0 resets) the device-side error word of the current device:
  * 0 when no kernel gave up on a bounded wait.  Synchronises `stream`.  Bits: 1, 2, 4 -- a GEMM
  * wait (producer, tensor-core issue, epilogue); 8 -- a weight-fold copy; 16 -- an activation-row

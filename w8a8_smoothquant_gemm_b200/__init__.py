@@ -11,6 +11,8 @@ Pipeline ("4.2 W8A8 量化与 SmoothQuant", sec. 7.1):
   runtime:  sq_ln_smooth_quant -> sq_w8a8_gemm
 FP8 (E4M3) variant of the quantised steps: sq_fold_quant_weights_fp8, sq_ln_smooth_quant_fp8,
 sq_w8a8_gemm_fp8.
+Weight-only 4-bit variant for a few tokens: sq_fold_quant_weights_w4, sq_w4_gemm, sq_w4_dequant,
+and mixture-of-experts layers of such weights: sq_moe_w4, sq_moe_w4_routed.
 """
 from __future__ import annotations
 
@@ -66,6 +68,11 @@ def lib() -> ctypes.CDLL:
             "sq_w8a8_gemm_rowmax": [P, P, P, P, I64, I64, I64, P, I, I64, P, P, SZ, P],
             "sq_quant_codes": [P, I, I64, I64, I64, P, P, P, P],
             "sq_set_wait_limit": [ctypes.c_uint64, P],
+            "sq_fold_quant_weights_w4": [P, I, I64, I64, I64, P, P, P, I, P, P, P, P, P, P],
+            "sq_w4_dequant": [P, P, P, I64, I64, I, P, I, I64, P],
+            "sq_w4_gemm": [P, I, I64, I64, I64, P, P, P, I64, I, P, I, I64, P],
+            "sq_moe_w4": [P, I, I64, I64, I64, P, I, I64, I, I, P, P, P, P, P, P, P, P, I64, I, P, I, I64, P, SZ, P],
+            "sq_moe_w4_routed": [P, I, I64, I64, I64, P, P, I64, I, P, P, P, P, P, P, I64, I, P, I, I64, P, SZ, P],
         }
         for name, argt in sigs.items():
             fn = getattr(L, name)
@@ -75,6 +82,10 @@ def lib() -> ctypes.CDLL:
         L.sq_w8a8_gemm_workspace_size.restype = SZ
         L.sq_alpha_search_workspace_size.argtypes = [I64, I64, I64]
         L.sq_alpha_search_workspace_size.restype = SZ
+        L.sq_moe_w4_workspace_size.argtypes = [I64, I64, I64, I64, I]
+        L.sq_moe_w4_workspace_size.restype = SZ
+        L.sq_w4_row_bytes.argtypes = [I64]
+        L.sq_w4_row_bytes.restype = I64
         L.sq_status_string.argtypes = [I]
         L.sq_status_string.restype = ctypes.c_char_p
         L.sq_abi_version.argtypes = []
@@ -450,6 +461,197 @@ def sq_selfcheck_shared_divisor(a: torch.Tensor, b: torch.Tensor, want_quotients
     _check("sq_selfcheck_shared_divisor", lib().sq_selfcheck_shared_divisor(_ptr(a), a.numel(), _ptr(b), b.numel(),
                                                                             _ptr(q), _ptr(counts), _stream(stream)))
     return counts, q
+
+
+# ----------------------------------------------------------------------------- 4-bit weights
+# A packed weight is (wq [N, sq_w4_row_bytes(K)] uint8, sg [ceil(K / group), N] bfloat16, zp uint8
+# like sg or None); experts stack these on a leading dimension.  Calls run on the tensors' own
+# device: its current stream is taken unless `stream` is given.
+def sq_w4_row_bytes(K: int) -> int:
+    return (K + 127) // 128 * 64
+
+
+def _on(dev: torch.device, stream):
+    """The stream to launch on, and the device switch it needs (None where it is current already)."""
+    if dev.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    cur = torch.cuda.current_device()
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError("the stream belongs to another device than the tensors")
+        raw = stream.cuda_stream
+    else:
+        raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    return raw, None if dev.index == cur else torch.cuda.device(dev)
+
+
+def _call(fn: str, dev: torch.device, stream, *args):
+    raw, switch = _on(dev, stream)
+    f = getattr(_lib or lib(), fn)
+    if switch is None:
+        status = f(*args, raw)
+    else:
+        with switch:
+            status = f(*args, raw)
+    if status != 0:
+        raise SQError(fn, status)
+
+
+def _packed(name: str, wq, sg, zp, lead: tuple, K: int, group: int, dev):
+    """Checks one packed weight: codes [*lead, row bytes], scales (and zero points) [.., groups, N]."""
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    gshape = (*lead[:-1], (K + group - 1) // group, lead[-1])
+    if wq.dtype != torch.uint8 or wq.shape != (*lead, sq_w4_row_bytes(K)) or not wq.is_contiguous() or wq.device != dev:
+        raise ValueError(f"{name}: codes must be contiguous uint8 {(*lead, sq_w4_row_bytes(K))} on the input's device")
+    if sg.dtype != torch.bfloat16 or sg.shape != gshape or not sg.is_contiguous() or sg.device != dev:
+        raise ValueError(f"{name}: scales must be contiguous bfloat16 {gshape} on the input's device")
+    if zp is not None and (zp.dtype != torch.uint8 or zp.shape != gshape or not zp.is_contiguous() or zp.device != dev):
+        raise ValueError(f"{name}: zero points must be contiguous uint8 {gshape} on the input's device")
+
+
+def _ptr0(t):
+    return None if t is None else t.data_ptr()
+
+
+def _out(y, shape: tuple, dtype, dev):
+    if y is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if y.shape != shape or y.device != dev or y.stride(-1) != 1:
+        raise ValueError(f"y must be {shape} with unit column stride, on the input's device")
+    return y
+
+
+def _odt(t: torch.Tensor) -> int:
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"expected a bfloat16 or float32 output, got {t.dtype}")
+    return SQ_BF16 if t.dtype == torch.bfloat16 else SQ_F32
+
+
+def sq_fold_quant_weights_w4(W: torch.Tensor, s: torch.Tensor | None = None, gamma: torch.Tensor | None = None,
+                             beta: torch.Tensor | None = None, group: int = 128, asym: bool = False,
+                             wq: torch.Tensor | None = None, sg: torch.Tensor | None = None,
+                             zp: torch.Tensor | None = None, stream=None):
+    """W [K, N] -> (wq packed, sg, zp or None, gamma / s or None, beta / s or None).  asym: with zero points."""
+    W = _mat(W, "W")
+    K, N = W.shape
+    dev = W.device
+    for v, name in ((s, "s"), (gamma, "gamma"), (beta, "beta")):
+        _vec(v, K, name)
+        if v is not None and v.device != dev:
+            raise ValueError(f"{name} must be on W's device")
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    groups = (K + group - 1) // group
+    wq = torch.empty(N, sq_w4_row_bytes(K), dtype=torch.uint8, device=dev) if wq is None else wq
+    sg = torch.empty(groups, N, dtype=torch.bfloat16, device=dev) if sg is None else sg
+    if not asym and zp is not None:
+        raise ValueError("zero points are written only with asym=True")
+    if asym and zp is None:
+        zp = torch.empty(groups, N, dtype=torch.uint8, device=dev)
+    _packed("W", wq, sg, zp, (N,), K, group, dev)
+    gf = torch.empty_like(gamma) if gamma is not None else None
+    bf = torch.empty_like(beta) if beta is not None else None
+    _call("sq_fold_quant_weights_w4", dev, stream, W.data_ptr(), _dt(W), K, N, W.stride(0), _ptr0(s), _ptr0(gamma),
+          _ptr0(beta), group, wq.data_ptr(), sg.data_ptr(), _ptr0(zp), _ptr0(gf), _ptr0(bf))
+    return wq, sg, zp, gf, bf
+
+
+def sq_w4_dequant(wq: torch.Tensor, sg: torch.Tensor, zp: torch.Tensor | None = None, *, K: int, group: int = 128,
+                  out_dtype: torch.dtype = torch.bfloat16, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values [N, K] that a packed weight stands for: (code - zero) * scale."""
+    if wq.dim() != 2:
+        raise ValueError("wq must be 2-D")
+    N, dev = wq.shape[0], wq.device
+    _packed("wq", wq, sg, zp, (N,), K, group, dev)
+    y = _out(y, (N, K), out_dtype, dev)
+    _call("sq_w4_dequant", dev, stream, wq.data_ptr(), sg.data_ptr(), _ptr0(zp), K, N, group, y.data_ptr(), _odt(y),
+          y.stride(0))
+    return y
+
+
+def sq_w4_gemm(x: torch.Tensor, wq: torch.Tensor, sg: torch.Tensor, zp: torch.Tensor | None = None, group: int = 128,
+               out_dtype: torch.dtype = torch.bfloat16, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y [M, N] = x [M, K] @ values(wq, sg, zp) [N, K]^T, for a few tokens."""
+    x = _mat(x, "x")
+    M, K = x.shape
+    N, dev = wq.shape[0], x.device
+    _packed("wq", wq, sg, zp, (N,), K, group, dev)
+    y = _out(y, (M, N), out_dtype, dev)
+    _call("sq_w4_gemm", dev, stream, x.data_ptr(), _dt(x), M, K, x.stride(0), wq.data_ptr(), sg.data_ptr(), _ptr0(zp), N,
+          group, y.data_ptr(), _odt(y), y.stride(0))
+    return y
+
+
+def sq_moe_w4_workspace_size(T: int, D: int, F: int, E: int, top_k: int) -> int:
+    n = int(lib().sq_moe_w4_workspace_size(T, D, F, E, top_k))
+    if n == (1 << 64) - 1:
+        raise ValueError("sizes outside the mixture-of-experts layer's limits")
+    return n
+
+
+def sq_moe_w4_workspace(T: int, D: int, F: int, E: int, top_k: int, device="cuda") -> torch.Tensor:
+    """A workspace for sq_moe_w4 and sq_moe_w4_routed, for these sizes and smaller ones; calls that share it must be
+    ordered."""
+    return torch.zeros(sq_moe_w4_workspace_size(T, D, F, E, top_k), dtype=torch.uint8, device=device)
+
+
+def _moe(fn, x, E, k, route, w13, s13, w2, s2, z13, z2, group, out_dtype, y, workspace, stream):
+    T, D = x.shape
+    dev = x.device
+    if w13.dim() != 3 or w13.shape[1] % 2:
+        raise ValueError("w13 must be [E, 2 F, row bytes]")
+    F = w13.shape[1] // 2
+    if (z13 is None) != (z2 is None):
+        raise ValueError("zero points are given for both weights or for neither")
+    _packed("w13", w13, s13, z13, (E, 2 * F), D, group, dev)
+    _packed("w2", w2, s2, z2, (E, D), F, group, dev)
+    y = _out(y, (T, D), out_dtype, dev)
+    if workspace is None:
+        workspace = sq_moe_w4_workspace(T, D, F, E, k, dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous and on the input's device")
+    _call(fn, dev, stream, x.data_ptr(), _dt(x), T, D, x.stride(0), *route, w13.data_ptr(), s13.data_ptr(), _ptr0(z13),
+          w2.data_ptr(), s2.data_ptr(), _ptr0(z2), F, group, y.data_ptr(), _odt(y), y.stride(0), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+    return y
+
+
+def sq_moe_w4(x: torch.Tensor, wr: torch.Tensor, top_k: int, w13: torch.Tensor, s13: torch.Tensor, w2: torch.Tensor,
+              s2: torch.Tensor, z13: torch.Tensor | None = None, z2: torch.Tensor | None = None, group: int = 128,
+              renorm: bool = True, out_dtype: torch.dtype = torch.bfloat16, y: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None, stream=None):
+    """A mixture-of-experts layer for a few tokens: router wr [E, D], the top_k experts of each token (softmax
+    weights, divided by their sum if renorm), silu(gate) * up, weighted sum.  Returns (y [T, D], ids [T, top_k]
+    int32, weights [T, top_k] float32).  workspace: sq_moe_w4_workspace, made for the call if not given."""
+    x = _mat(x, "x")
+    wr = _mat(wr, "wr")
+    T, E = x.shape[0], wr.shape[0]
+    if wr.shape[1] != x.shape[1] or not wr.is_contiguous() or wr.device != x.device:
+        raise ValueError("wr must be contiguous [E, D] on the input's device")
+    if not 0 < top_k <= E:
+        raise ValueError("top_k must be between 1 and the number of experts")
+    ids = torch.empty(T, top_k, dtype=torch.int32, device=x.device)
+    wts = torch.empty(T, top_k, dtype=torch.float32, device=x.device)
+    y = _moe("sq_moe_w4", x, E, top_k, (wr.data_ptr(), _dt(wr), E, top_k, int(renorm), ids.data_ptr(), wts.data_ptr()),
+             w13, s13, w2, s2, z13, z2, group, out_dtype, y, workspace, stream)
+    return y, ids, wts
+
+
+def sq_moe_w4_routed(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor,
+                     w2: torch.Tensor, s2: torch.Tensor, z13: torch.Tensor | None = None,
+                     z2: torch.Tensor | None = None, group: int = 128, out_dtype: torch.dtype = torch.bfloat16,
+                     y: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The experts of sq_moe_w4 for given choices: ids [T, top_k] int32 (outside [0, E): left out) and weights
+    [T, top_k] float32."""
+    x = _mat(x, "x")
+    T, E = x.shape[0], w13.shape[0]
+    k = ids.shape[-1]
+    for v, dt, name in ((ids, torch.int32, "ids"), (weights, torch.float32, "weights")):
+        if v.dtype != dt or v.shape != (T, k) or not v.is_contiguous() or v.device != x.device:
+            raise ValueError(f"{name} must be contiguous {dt} [T, top_k] on the input's device")
+    return _moe("sq_moe_w4_routed", x, E, k, (ids.data_ptr(), weights.data_ptr(), E, k), w13, s13, w2, s2, z13, z2, group,
+                out_dtype, y, workspace, stream)
 
 
 WAIT_LIMIT_DEFAULT_NS = 10 * 1000 * 1000 * 1000
