@@ -372,7 +372,8 @@ sq_status sq_w4_gemm(const void* x, sq_dtype dt, int64_t M, int64_t K, int64_t l
  *   x: [T, D] bf16/fp32, ldx, 16-byte aligned rows; Wr: [E, D] dense bf16/fp32 (rdt), 16-byte aligned.
  *   W13: [E, 2 F, sq_w4_row_bytes(D)] packed, the F rows of W1 (gate) first, then the F rows of W3
  *   (up); s13: bf16 [E, ceil(D / group), 2 F].  W2: [E, D, sq_w4_row_bytes(F)]; s2:
- *   [E, ceil(F / group), D].  z13, z2: zero points shaped like the scales, both or neither.
+ *   [E, ceil(F / group), D].  z13, z2: zero points shaped like the scales, both or neither.  All
+ *   six are 16-byte aligned.
  *   ids: int32 [T, top_k], weights: fp32 [T, top_k], written.  y: [T, D], ldy >= D.
  *   D % 16 == 0, F % 16 == 0, both <= SQ_MAX_K; T <= SQ_MOE_MAX_TOKENS (more: SQ_ERR_UNSUPPORTED).
  *   workspace: sq_moe_w4_workspace_size(T, D, F, E, top_k) bytes, 256-byte aligned, zero-filled

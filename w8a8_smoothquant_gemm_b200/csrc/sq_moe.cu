@@ -11,7 +11,8 @@
 //   Router sums are binary64, so that which experts are chosen does not hang on rounding.  h is
 // kept as two bf16 parts (16 significant bits; three for a binary32 layer), so the only bf16
 // rounding of the layer is the final store.  Every sum has a fixed order; the only atomics are the
-// lists' bit masks (order-free) and the router's arrival count.
+// lists' bit masks (order-free) and the router's arrival count.  The expert kernels are one CTA per
+// SM with the weight stream of sq_w4.cuh.
 #include <algorithm>
 
 #include "sq_w4.cuh"
@@ -22,10 +23,11 @@ constexpr int MOE_MAX_T = 64;    // tokens: one bit each of an expert's token ma
 constexpr int MOE_MAX_E = 1024;  // experts
 constexpr int MOE_MAX_K = 32;    // choices per token
 constexpr int MOE_THREADS = 256;
+constexpr int MOE_ENTRY = 32;    // tokens of an entry: four column tiles of the mma
 
 struct MoeLists {  // in the workspace, written by the router (or from given choices)
   unsigned int arrived;  // router blocks that are done; wraps to 0 by itself
-  int active;            // experts with tokens
+  int active;            // entries: experts with tokens, MOE_ENTRY of them at a time
 };
 
 struct MoeParams {
@@ -50,11 +52,15 @@ struct MoeParams {
   MoeLists* lists;
   double* logits;       // [T, E]
   int* expert;          // [active] expert of an entry
-  int* start;           // [active + 1] its first slot
+  int* start;           // [active + 1] its first slot; the slots of an expert's entries follow one another
   int* slot_token;      // [T k]
   float* slot_weight;   // [T k]
   uint16_t* xparts;     // [3, T, D] (binary32 x)
   uint16_t* h;          // [parts, T k, F]
+  // the expert kernels' shared memory
+  bool x_staged;        // x in shared memory
+  int up_cells_at, up_ring_at, up_pass;  // tiles whose cells fit
+  int down_ring_at, down_pass;
   int C;                // CTAs of the down kernel's cluster
 };
 
@@ -77,15 +83,15 @@ __device__ void moe_build_lists(const MoeParams& p, MoeShared& sh, const int* id
     if (e >= 0 && e < p.E) atomicOr(&sh.mask[e], 1ull << (i / p.top_k));
   }
   __syncthreads();
-  // exclusive sums of tokens and of active experts: a run of experts per thread, then a scan
+  // exclusive sums of tokens and of entries: a run of experts per thread, then a scan
   const int per = (p.E + MOE_THREADS - 1) / MOE_THREADS;
   int tokens = 0, active = 0;
   for (int e = tid * per; e < min(p.E, (tid + 1) * per); ++e) {
     const int c = __popcll(sh.mask[e]);
     tokens += c;
-    active += c > 0;
+    active += (c + MOE_ENTRY - 1) / MOE_ENTRY;
   }
-  int packed = tokens | (active << 16);  // at most 2048 slots and 1024 experts
+  int packed = tokens | (active << 16);  // at most 2048 slots and as many entries
   sh.scan[tid] = packed;
   __syncthreads();
   for (int o = 1; o < MOE_THREADS; o *= 2) {
@@ -100,12 +106,12 @@ __device__ void moe_build_lists(const MoeParams& p, MoeShared& sh, const int* id
   for (int e = tid * per; e < min(p.E, (tid + 1) * per); ++e) {
     const int c = __popcll(sh.mask[e]);
     sh.offset[e] = tokens;
-    if (c > 0) {
+    for (int first = 0; first < c; first += MOE_ENTRY) {
       p.expert[active] = e;
-      p.start[active] = tokens;
+      p.start[active] = tokens + first;
       ++active;
-      tokens += c;
     }
+    tokens += c;
   }
   if (tid == MOE_THREADS - 1) {
     const int total = sh.scan[tid];
@@ -276,190 +282,317 @@ __global__ void __launch_bounds__(256) moe_split_kernel(const MoeParams p) {
   }
 }
 
-// ---------------------------------------------------------------------------- gate and up
-__device__ __forceinline__ uint4 ld_parts(const char* row, int64_t k, int64_t K) {
+// ---------------------------------------------------------------------------- experts
+constexpr int MOE_DEPTH = 3;   // slots of a warp's ring
+constexpr int MOE_WARPS = 16;  // of an expert kernel's CTA
+constexpr int MOE_EXPERT_THREADS = 32 * MOE_WARPS;
+constexpr int MOE_NT = MOE_ENTRY / 8;
+
+// The 8 values at k of a row of x or h (shared or global memory); zeros past its end.
+__device__ __forceinline__ uint4 moe_row8(const char* row, int k, int K) {
   return k < K ? *reinterpret_cast<const uint4*>(row + k * 2) : make_uint4(0, 0, 0, 0);
 }
 
-constexpr int MOE_DEPTH = 4;
-
-// Blocks [b0, b1) in steps of `step`, `depth` of them in flight.
-template <int NT, int S, int GW, bool ASYM>
-__device__ __forceinline__ void moe_run(float (&acc)[NT][4], const W4Rows& r, const char* const (&rows)[NT],
-                                        int64_t plane_bytes, int b0, int b1, int step, int64_t K, int lane) {
-  const int t = lane % 4;
-  W4Block w[MOE_DEPTH];
-#pragma unroll
-  for (int u = 0; u < MOE_DEPTH; ++u)
-    if (b0 + u * step < b1) w4_load<GW, ASYM>(w[u], r, b0 + u * step, t);
-  for (int bb = b0; bb < b1; bb += step * MOE_DEPTH) {
-#pragma unroll
-    for (int u = 0; u < MOE_DEPTH; ++u) {
-      const int b = bb + u * step;
-      if (b < b1) {
-        w4_mac<NT, S, GW, ASYM>(acc, w[u], lane, [&](int n, int s, int i) {
-          return ld_parts(rows[n] + s * plane_bytes, (int64_t)b * W4_BLOCK + 32 * i + 8 * t, K);
-        });
-        if (b + step * MOE_DEPTH < b1) w4_load<GW, ASYM>(w[u], r, b + step * MOE_DEPTH, t);
-      }
-    }
-  }
+// One unit for an entry of `count` tokens: as many column tiles as they need.
+template <int S, int GW, bool ASYM>
+__device__ __forceinline__ void moe_mac(float (&acc)[MOE_NT][4], uint32_t slot, int lane, int count,
+                                        const char* const (&rows)[MOE_NT], int64_t plane, int b, int K) {
+  const int k0 = b * W4_UNIT + (lane % 4) * 8;
+  auto x = [&](int n, int s, int i) { return moe_row8(rows[n] + s * plane, k0 + 32 * i, K); };
+  if (count <= 8) w4_mac<1, S, GW, ASYM>(acc, slot, lane, x);
+  else if (count <= 16) w4_mac<2, S, GW, ASYM>(acc, slot, lane, x);
+  else w4_mac<4, S, GW, ASYM>(acc, slot, lane, x);
 }
 
-// Item: 8 rows f of one expert's gate and the same 8 of its up projection, as the two halves of a
-// 16-row tile, so one thread ends up with both sums of an h.  The block's 8 warps split D.
-template <int NT, int S, int SH, int GW, bool ASYM>
-__device__ __forceinline__ void moe_up_tile(const MoeParams& p, float* red, int e, int f0, int slot0, int count) {
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
-  const int nb = (int)w4_blocks(p.D);
-  W4Rows r;
-  const int f = min(f0 + g, p.F - 1);
-  const int64_t row = (int64_t)e * 2 * p.F + f;
-  r.lo = p.w13 + row * p.rb13 + t * 16;
-  r.hi = p.w13 + (row + p.F) * p.rb13 + t * 16;
-  const int64_t sbase = (int64_t)e * p.g13 * 2 * p.F + f;
-  r.slo = p.s13 + sbase;
-  r.shi = p.s13 + sbase + p.F;
-  r.zlo = p.z13 + (ASYM ? sbase : 0);
-  r.zhi = p.z13 + (ASYM ? sbase + p.F : 0);
-  r.pitch = 2 * (int64_t)p.F;
-  r.last = p.g13 - 1;
-  const char* rows[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int tok = p.slot_token[slot0 + min(8 * n + g, count - 1)];
-    rows[n] = S == 1 ? p.x + tok * p.ldx_bytes : reinterpret_cast<const char*>(p.xparts) + (int64_t)tok * p.D * 2;
-  }
-  float acc[NT][4];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-  moe_run<NT, S, GW, ASYM>(acc, r, rows, (int64_t)p.T * p.D * 2, warp, nb, 8, p.D, lane);
-  __syncthreads();  // the last tile's sums have been read
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) red[((n * 4 + i) * 8 + warp) * 32 + lane] = acc[n][i];
-  __syncthreads();
-  for (int o = tid; o < NT * 64; o += MOE_THREADS) {  // (column 8 n + 2 q + c, row gg) of lane gg * 4 + q
-    const int n = o / 64, c = o / 32 % 2, l = o % 32, col = 8 * n + 2 * (l % 4) + c, ff = f0 + l / 4;
-    float gate = 0.0f, up = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      gate = __fadd_rn(gate, red[((n * 4 + c) * 8 + k) * 32 + l]);
-      up = __fadd_rn(up, red[((n * 4 + 2 + c) * 8 + k) * 32 + l]);
+// Gate and up: a tile is 8 rows f of an entry's gate and the same 8 of its up projection, as the two
+// halves of a 16-row tile, so one thread finds both sums of an h.  The tiles of all entries are one
+// line, cut over the CTAs and there over the warps (sq_w4.cuh).
+template <int S, int SH, int GW, bool ASYM>
+__global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_up_kernel(const MoeParams p) {
+  constexpr int SLOT = W4Slot<GW, ASYM>::BYTES, RP = W4_RP;
+  extern __shared__ __align__(16) char smem[];
+  __shared__ W4Runs<MOE_WARPS> runs;
+  const int tid = threadIdx.x, lane = tid % 32, g = lane / 4, t = lane % 4;
+  const int warp = __shfl_sync(0xffffffffu, tid / 32, 0);
+  const int cell_floats = min(p.T, MOE_ENTRY) * RP;
+  float* cells = reinterpret_cast<float*>(smem + p.up_cells_at);
+  const uint32_t ring = smem_u32(smem + p.up_ring_at) + warp * MOE_DEPTH * SLOT;
+  const int nb = w4_units(p.D), per_expert = p.F / 8;
+  wait_for_previous_kernel();
+  allow_dependent_launch();
+  const int64_t tiles = (int64_t)p.lists->active * per_expert;
+  const int64_t t0 = tiles * blockIdx.x / gridDim.x;
+  const int my_tiles = (int)(tiles * (blockIdx.x + 1) / gridDim.x - t0);
+  const char* xbase = S == 1 ? p.x : reinterpret_cast<const char*>(p.xparts);
+  const int64_t xpitch = S == 1 ? p.ldx_bytes : (int64_t)p.D * 2;
+  const int64_t xplane = S == 1 ? 0 : (int64_t)p.T * p.D * 2;
+  const int spitch = (int)w4_blocks(p.D) * 256 + 64;  // rows 64 bytes apart modulo 128
+
+  for (int p0 = 0; p0 < my_tiles; p0 += p.up_pass) {
+    const int n_tiles = min(p.up_pass, my_tiles - p0), line = n_tiles * nb;
+    if (p0 != 0) __syncthreads();  // the last pass's cells have been read
+    else if (p.x_staged) {
+      for (int m = 0; m < S * p.T; ++m) {
+        const char* src = xbase + (m % p.T) * xpitch + m / p.T * xplane;
+        for (int v = tid; v < p.D / 8; v += MOE_EXPERT_THREADS) cp_async16(smem_u32(smem + m * spitch + v * 16), src + v * 16);
+      }
     }
-    if (col < count && ff < p.F) {
+    cp_commit();
+    const W4Run run = w4_runs<MOE_WARPS>(runs, line, nb, warp, lane);
+    int tile = run.tile, b = run.b;
+    float* cell = cells + run.cell * cell_floats + g;
+
+    W4Base base{};
+    base.row_bytes = (uint32_t)p.rb13;
+    base.pitch = 2 * p.F;
+    base.groups = p.g13;
+    auto place = [&](int ti, int at_b) {
+      const int64_t at = t0 + p0 + ti;
+      const int a = (int)(at / per_expert), f0 = (int)(at - (int64_t)a * per_expert) * 8;
+      const int64_t e = p.expert[a];
+      base.codes = p.w13 + e * 2 * p.F * p.rb13;
+      base.scales = p.s13 + e * p.g13 * 2 * p.F;
+      if (ASYM) base.zeros = p.z13 + e * p.g13 * 2 * p.F;
+      return w4_place<GW, ASYM, true>(base, f0, p.F + f0, 2 * p.F - 1, at_b, lane);
+    };
+    int to_load = run.units, load_tile = tile, load_b = b;
+    W4Cursor cur{};
+    if (to_load > 0) cur = place(tile, b);
+    const bool odd = w4_blocks(p.D) % 2 != 0;  // the last unit of a row is half a one
+    auto issue = [&](uint32_t into) {
+      if (to_load > 0) {
+        w4_issue<GW, ASYM, true>(into, base, cur, odd && load_b == nb - 1, lane);
+        --to_load;
+        if (++load_b == nb) {
+          load_b = 0;
+          ++load_tile;
+          if (to_load > 0) cur = place(load_tile, 0);
+        }
+      }
+      cp_commit();
+    };
+#pragma unroll 1
+    for (int u = 0; u < MOE_DEPTH - 1; ++u) issue(ring + u * SLOT);
+    cp_wait<MOE_DEPTH - 1>();  // x; the ring's blocks are younger
+    __syncthreads();
+
+    float acc[MOE_NT][4] = {};
+    const char* rows[MOE_NT];
+    int count = 0;
+    bool begin = true;
+    uint32_t slot = ring, spent = ring + (MOE_DEPTH - 1) * SLOT;
+    for (int left = run.units; left > 0; --left) {
+      if (begin) {
+        const int a = (int)((t0 + p0 + tile) / per_expert), s0 = p.start[a];
+        count = p.start[a + 1] - s0;
+#pragma unroll
+        for (int n = 0; n < MOE_NT; ++n) {
+          const int tok = p.slot_token[s0 + min(8 * n + g, count - 1)];
+          rows[n] = p.x_staged ? smem + tok * spitch : xbase + tok * xpitch;
+        }
+        begin = false;
+      }
+      cp_wait<MOE_DEPTH - 2>();
+      __syncwarp();
+      issue(spent);
+      moe_mac<S, GW, ASYM>(acc, slot, lane, count, rows, p.x_staged ? (int64_t)p.T * spitch : xplane, b, p.D);
+      spent = slot;
+      slot = slot == ring + (MOE_DEPTH - 1) * SLOT ? ring : slot + SLOT;
+      if (++b == nb || left == 1) {
+#pragma unroll
+        for (int n = 0; n < MOE_NT; ++n) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int m = 8 * n + 2 * t + c;
+            if (m < count) {
+              cell[m * RP] = acc[n][c];
+              cell[m * RP + 8] = acc[n][2 + c];
+            }
+            acc[n][c] = acc[n][2 + c] = 0.0f;
+          }
+        }
+        cell += cell_floats;
+        b = 0;
+        ++tile;
+        begin = true;
+      }
+    }
+    __syncthreads();
+    const int cols = min(p.T, MOE_ENTRY);
+    const float inv_line = __frcp_rn((float)line);
+    for (int o = tid; o < n_tiles * cols * 8; o += MOE_EXPERT_THREADS) {
+      const int f = o % 8, mt = o / 8, ti = mt / cols, m = mt - ti * cols;
+      const int64_t at = t0 + p0 + ti;
+      const int a = (int)(at / per_expert), s0 = p.start[a];
+      if (m >= p.start[a + 1] - s0) continue;
+      const float* q = cells + m * RP + f;
+      float gate = 0.0f, up = 0.0f;
+      w4_cells_of<MOE_WARPS>(runs, ti, line, inv_line, nb, [&](int c) {
+        gate = __fadd_rn(gate, q[c * cell_floats]);
+        up = __fadd_rn(up, q[c * cell_floats + 8]);
+      });
       // silu(v) = v / (1 + exp(-v)); exp overflows to inf for very negative v, and v / inf is -0
       const float h = __fmul_rn(__fdiv_rn(gate, __fadd_rn(1.0f, expf(-gate))), up);
       uint32_t part[SH];
       split_bf16_stored<SH>(h, part);
+      const int64_t ff = (at - (int64_t)a * per_expert) * 8 + f;
 #pragma unroll
-      for (int s = 0; s < SH; ++s)
-        p.h[((int64_t)s * p.T * p.top_k + slot0 + col) * p.F + ff] = (uint16_t)part[s];
+      for (int s = 0; s < SH; ++s) p.h[((int64_t)s * p.T * p.top_k + s0 + m) * p.F + ff] = (uint16_t)part[s];
     }
   }
 }
 
-template <int S, int SH, int GW, bool ASYM>
-__global__ void __launch_bounds__(MOE_THREADS) moe_up_kernel(const MoeParams p) {
-  __shared__ float red[2 * 4 * 8 * 32];
+// Down: a tile is 16 rows d; its blocks are those of every entry in turn (a rank of a cluster takes
+// a share of that line, where there are few tiles).  A cell holds sums for every token, to which an
+// entry's are added with the tokens' weights when the warp leaves the entry.
+template <int SH, int GW, bool ASYM>
+__global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_down_kernel(const MoeParams p) {
+  constexpr int SLOT = W4Slot<GW, ASYM>::BYTES, RP = W4_RP;
+  extern __shared__ __align__(16) char smem[];
+  __shared__ W4Runs<MOE_WARPS> runs;
+  const int tid = threadIdx.x, lane = tid % 32, g = lane / 4, t = lane % 4;
+  const int warp = __shfl_sync(0xffffffffu, tid / 32, 0);
+  const int cell_floats = p.T * RP;
+  float* cells = reinterpret_cast<float*>(smem);
+  const uint32_t ring = smem_u32(smem + p.down_ring_at) + warp * MOE_DEPTH * SLOT;
+  float* out = reinterpret_cast<float*>(smem + p.down_ring_at);  // [tile][token][row] over the ranks, after the rings
+  const int nb = w4_units(p.F);
+  const int rank = blockIdx.x % p.C, cluster = blockIdx.x / p.C, clusters = gridDim.x / p.C;
+  const int tiles = (p.D + 15) / 16, t0 = (int)((int64_t)tiles * cluster / clusters);
+  const int my_tiles = (int)((int64_t)tiles * (cluster + 1) / clusters) - t0;
   wait_for_previous_kernel();
   allow_dependent_launch();
-  const int tiles = (p.F + 7) / 8;
-  const int items = p.lists->active * tiles;
-  for (int i = blockIdx.x; i < items; i += gridDim.x) {
-    const int a = i / tiles, e = p.expert[a], f0 = (i % tiles) * 8;
-    const int s1 = p.start[a + 1];
-    for (int s0 = p.start[a]; s0 < s1; s0 += 16) {
-      if (s1 - s0 <= 8) moe_up_tile<1, S, SH, GW, ASYM>(p, red, e, f0, s0, s1 - s0);
-      else moe_up_tile<2, S, SH, GW, ASYM>(p, red, e, f0, s0, min(16, s1 - s0));
-    }
-  }
-}
+  const int all = p.lists->active * nb, first = (int)((int64_t)all * rank / p.C);
+  const int per_tile = (int)((int64_t)all * (rank + 1) / p.C) - first;
+  const int64_t plane = (int64_t)p.T * p.top_k * p.F * 2;
 
-// ---------------------------------------------------------------------------- down
-template <int NT, int SH, int GW, bool ASYM>
-__device__ __forceinline__ void moe_down_part(const MoeParams& p, float* mine, int e, int d0, int slot0, int count,
-                                              int b0, int b1) {
-  const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  W4Rows r;
-  const int lo = min(d0 + g, p.D - 1), hi = min(d0 + g + 8, p.D - 1);
-  r.lo = p.w2 + ((int64_t)e * p.D + lo) * p.rb2 + t * 16;
-  r.hi = p.w2 + ((int64_t)e * p.D + hi) * p.rb2 + t * 16;
-  const int64_t sbase = (int64_t)e * p.g2 * p.D;
-  r.slo = p.s2 + sbase + lo;
-  r.shi = p.s2 + sbase + hi;
-  r.zlo = p.z2 + (ASYM ? sbase + lo : 0);
-  r.zhi = p.z2 + (ASYM ? sbase + hi : 0);
-  r.pitch = p.D;
-  r.last = p.g2 - 1;
-  const char* rows[NT];
+  for (int p0 = 0; p0 < my_tiles; p0 += p.down_pass) {
+    const int n_tiles = min(p.down_pass, my_tiles - p0), line = n_tiles * per_tile;
+    if (p0 != 0) __syncthreads();
+    if (line > 0) {
+      const W4Run run = w4_runs<MOE_WARPS>(runs, line, per_tile, warp, lane);
+        int tile = run.tile, at = run.b;  // block of the tile's line
+      int a = (first + at) / nb, b = first + at - a * nb;
+      float* cell = cells + run.cell * cell_floats;
+
+      W4Base base{};
+      base.row_bytes = (uint32_t)p.rb2;
+      base.pitch = p.D;
+      base.groups = p.g2;
+        auto place = [&](int ti, int entry, int at_b) {
+        const int64_t e = p.expert[entry];
+        base.codes = p.w2 + e * p.D * p.rb2;
+        base.scales = p.s2 + e * p.g2 * p.D;
+        if (ASYM) base.zeros = p.z2 + e * p.g2 * p.D;
+        const int row = (t0 + p0 + ti) * 16;
+        return w4_place<GW, ASYM, true>(base, row, row + 8, p.D - 1, at_b, lane);
+      };
+      int to_load = run.units, load_tile = tile, load_at = at, load_a = a, load_b = b;
+      W4Cursor cur{};
+      if (to_load > 0) cur = place(tile, a, b);
+      const bool odd = w4_blocks(p.F) % 2 != 0;  // the last unit of a row is half a one
+      auto issue = [&](uint32_t into) {
+        if (to_load > 0) {
+          w4_issue<GW, ASYM, true>(into, base, cur, odd && load_b == nb - 1, lane);
+          --to_load;
+          ++load_at;
+          if (++load_b == nb || load_at == per_tile) {
+            load_b = 0;
+            ++load_a;
+            if (load_at == per_tile) {
+              load_at = 0;
+              ++load_tile;
+              load_a = first / nb;
+              load_b = first - load_a * nb;
+            }
+            if (to_load > 0) cur = place(load_tile, load_a, load_b);
+          }
+        }
+        cp_commit();
+      };
+#pragma unroll 1
+      for (int u = 0; u < MOE_DEPTH - 1; ++u) issue(ring + u * SLOT);
+
+      float acc[MOE_NT][4] = {};
+      const char* rows[MOE_NT];
+      int s0 = 0, count = 0;
+      bool begin = true, fresh = true;
+      uint32_t slot = ring, spent = ring + (MOE_DEPTH - 1) * SLOT;
+      for (int left = run.units; left > 0; --left) {
+        if (fresh) {
+          for (int i = lane; i < cell_floats; i += 32) cell[i] = 0.0f;
+          __syncwarp();
+          fresh = false;
+        }
+        if (begin) {
+          s0 = p.start[a];
+          count = p.start[a + 1] - s0;
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-    rows[n] = reinterpret_cast<const char*>(p.h + (int64_t)(slot0 + min(8 * n + g, count - 1)) * p.F);
-  float acc[NT][4];
+          for (int n = 0; n < MOE_NT; ++n)
+            rows[n] = reinterpret_cast<const char*>(p.h + (int64_t)(s0 + min(8 * n + g, count - 1)) * p.F);
+          begin = false;
+        }
+        cp_wait<MOE_DEPTH - 2>();
+        __syncwarp();
+        issue(spent);
+        moe_mac<SH, GW, ASYM>(acc, slot, lane, count, rows, plane, b, p.F);
+        spent = slot;
+        slot = slot == ring + (MOE_DEPTH - 1) * SLOT ? ring : slot + SLOT;
+        ++at;
+        if (++b == nb || at == per_tile || left == 1) {
 #pragma unroll
-  for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-  moe_run<NT, SH, GW, ASYM>(acc, r, rows, (int64_t)p.T * p.top_k * p.F * 2, b0, b1, 1, p.F, lane);
+          for (int n = 0; n < MOE_NT; ++n) {
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int col = 8 * n + 2 * t + c;
-      if (col < count) {  // an expert's tokens differ, so no two lanes meet in a cell
-        const float w = p.slot_weight[slot0 + col];
-        float* cell = mine + p.slot_token[slot0 + col] * 16 + g;
-        cell[0] = __fmaf_rn(w, acc[n][c], cell[0]);
-        cell[8] = __fmaf_rn(w, acc[n][2 + c], cell[8]);
+            for (int c = 0; c < 2; ++c) {
+              const int m = 8 * n + 2 * t + c;
+              if (m < count) {  // an entry's tokens differ, so no two lanes meet in a place
+                const float w = p.slot_weight[s0 + m];
+                float* q = cell + p.slot_token[s0 + m] * RP + g;
+                q[0] = __fmaf_rn(w, acc[n][c], q[0]);
+                q[8] = __fmaf_rn(w, acc[n][2 + c], q[8]);
+              }
+              acc[n][c] = acc[n][2 + c] = 0.0f;
+            }
+          }
+          __syncwarp();
+          b = 0;
+          ++a;
+          begin = true;
+          if (at == per_tile) {
+            at = 0;
+            ++tile;
+            a = first / nb;
+            b = first - a * nb;
+            cell += cell_floats;
+            fresh = true;
+          }
+        }
       }
     }
-  }
-  __syncwarp();
-}
-
-// A cluster owns 16 rows d for every token; its warps cut the (expert, block) line into equal runs.
-template <int SH, int GW, bool ASYM>
-__global__ void __launch_bounds__(MOE_THREADS) moe_down_kernel(const MoeParams p) {
-  extern __shared__ __align__(16) float sums[];  // [8 warps][T][16]
-  const int tid = threadIdx.x, warp = tid / 32;
-  const int rank = blockIdx.x % p.C, d0 = blockIdx.x / p.C * 16;
-  const int cells = p.T * 16;
-  for (int i = tid; i < 8 * cells; i += MOE_THREADS) sums[i] = 0.0f;
-  wait_for_previous_kernel();
-  allow_dependent_launch();
-  __syncthreads();
-  const int nb = (int)w4_blocks(p.F);
-  const int64_t line = (int64_t)p.lists->active * nb;
-  const int runs = 8 * p.C, run = rank * 8 + warp;
-  const int64_t l1 = line * (run + 1) / runs;
-  for (int64_t l = line * run / runs; l < l1;) {
-    const int a = (int)(l / nb), b0 = (int)(l % nb), b1 = (int)min((int64_t)nb, b0 + (l1 - l));
-    const int e = p.expert[a], s1 = p.start[a + 1];
-    for (int s0 = p.start[a]; s0 < s1; s0 += 16) {
-      if (s1 - s0 <= 8) moe_down_part<1, SH, GW, ASYM>(p, sums + warp * cells, e, d0, s0, s1 - s0, b0, b1);
-      else moe_down_part<2, SH, GW, ASYM>(p, sums + warp * cells, e, d0, s0, min(16, s1 - s0), b0, b1);
+    __syncthreads();
+    const int outs = n_tiles * p.T * 16;
+    const float inv_line = __frcp_rn((float)max(line, 1));
+    for (int o = tid; o < outs; o += MOE_EXPERT_THREADS) {
+      const int row = o % 16, mt = o / 16, ti = mt / p.T, m = mt - ti * p.T;
+      float v = 0.0f;
+      if (line > 0)
+        w4_cells_of<MOE_WARPS>(runs, ti, line, inv_line, per_tile, [&](int c) { v = __fadd_rn(v, cells[c * cell_floats + m * RP + row]); });
+      const int d = (t0 + p0 + ti) * 16 + row;
+      if (p.C > 1) out[o] = v;
+      else if (d < p.D) store_out(p.y, m * p.ldy + d, v, p.y_bf16);
     }
-    l += b1 - b0;
-  }
-  __syncthreads();
-  for (int o = tid; o < cells; o += MOE_THREADS) {
-    float v = sums[o];
-#pragma unroll
-    for (int k = 1; k < 8; ++k) v = __fadd_rn(v, sums[k * cells + o]);
-    sums[o] = v;
-  }
-  if (p.C > 1) cluster_sync();
-  else __syncthreads();
-  for (int o = rank * MOE_THREADS + tid; o < cells; o += p.C * MOE_THREADS) {
-    const int t = o / 16, d = d0 + o % 16;
-    float v = sums[o];
     if (p.C > 1) {
-      v = ld_dsmem_f32(sums + o, 0);
-      for (int c = 1; c < p.C; ++c) v = __fadd_rn(v, ld_dsmem_f32(sums + o, c));
+      cluster_sync();
+      for (int o = rank * MOE_EXPERT_THREADS + tid; o < outs; o += p.C * MOE_EXPERT_THREADS) {
+        const int row = o % 16, mt = o / 16, ti = mt / p.T, m = mt - ti * p.T;
+        float v = ld_dsmem_f32(out + o, 0);
+        for (int c = 1; c < p.C; ++c) v = __fadd_rn(v, ld_dsmem_f32(out + o, c));
+        const int d = (t0 + p0 + ti) * 16 + row;
+        if (d < p.D) store_out(p.y, m * p.ldy + d, v, p.y_bf16);
+      }
+      cluster_sync();  // no CTA leaves, or reuses its sums, while they are read
     }
-    if (d < p.D) store_out(p.y, t * p.ldy + d, v, p.y_bf16);
   }
-  if (p.C > 1) cluster_sync();
 }
 
 }  // namespace sqk
@@ -467,11 +600,11 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_down_kernel(const MoeParams p
 namespace sqh {
 namespace {
 
-cudaError_t launch_dependent(const void* kern, unsigned gx, unsigned gy, size_t smem, int cluster,
+cudaError_t launch_dependent(const void* kern, unsigned gx, unsigned gy, unsigned threads, size_t smem, int cluster,
                              const sqk::MoeParams& p, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(gx, gy);
-  cfg.blockDim = dim3(sqk::MOE_THREADS);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -486,16 +619,57 @@ cudaError_t launch_dependent(const void* kern, unsigned gx, unsigned gy, size_t 
   return cudaLaunchKernelExC(&cfg, kern, args);
 }
 
+constexpr int64_t kSmemBudget = 226 * 1024;  // of 227 KB; the rest covers the static arrays
+
 template <int S, int SH, int GW, bool ASYM>
 cudaError_t launch_experts(sqk::MoeParams p, cudaStream_t st) {
-  const int sms = num_sms();
-  cudaError_t e = launch_dependent((const void*)sqk::moe_up_kernel<S, SH, GW, ASYM>, (unsigned)(4 * sms), 1, 0, 1, p, st);
+  const void* up = (const void*)sqk::moe_up_kernel<S, SH, GW, ASYM>;
+  const void* down = (const void*)sqk::moe_down_kernel<SH, GW, ASYM>;
+  for (const void* k : {up, down}) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBudget);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t ring = (int64_t)sqk::MOE_WARPS * sqk::MOE_DEPTH * sqk::W4Slot<GW, ASYM>::BYTES;
+  const int64_t sms = num_sms();
+  // gate and up: as many tiles a pass as a CTA can have, as far as their cells fit beside x, and x in
+  // shared memory if half the tiles (at least eight) still have cells
+  const int64_t per = ((int64_t)std::min(p.E, p.T * p.top_k) * (p.F / 8) + sms - 1) / sms;
+  const int64_t cell = (int64_t)std::min(p.T, sqk::MOE_ENTRY) * sqk::W4_RP * 4;
+  const int64_t x = (int64_t)S * p.T * (sqk::w4_blocks(p.D) * 256 + 64);
+  auto passes = [&](int64_t room, int64_t c, int64_t n) { return std::min(n, room / c - (sqk::MOE_WARPS - 1)); };
+  p.x_staged = passes(kSmemBudget - ring - x, cell, per) >= std::min<int64_t>(per, std::max<int64_t>(8, per / 2));
+  p.up_cells_at = p.x_staged ? (int)x : 0;
+  p.up_pass = (int)passes(kSmemBudget - ring - p.up_cells_at, cell, per);
+  p.up_ring_at = (int)(p.up_cells_at + (p.up_pass + sqk::MOE_WARPS - 1) * cell);
+  cudaError_t e = launch_dependent(up, (unsigned)sms, 1, sqk::MOE_EXPERT_THREADS, (size_t)(p.up_ring_at + ring), 1, p, st);
   if (e != cudaSuccess) return e;
-  const int tiles = (p.D + 15) / 16;
+
+  const int64_t tiles = (p.D + 15) / 16, cell2 = (int64_t)p.T * sqk::W4_RP * 4;
   p.C = 1;
-  while (p.C < 8 && tiles * p.C < 3 * sms) p.C *= 2;
-  const size_t smem = (size_t)8 * p.T * 16 * 4;
-  return launch_dependent((const void*)sqk::moe_down_kernel<SH, GW, ASYM>, (unsigned)(tiles * p.C), 1, smem, p.C, p, st);
+  while (p.C < 8 && tiles * p.C * 2 <= sms) p.C *= 2;
+  int64_t clusters = std::min<int64_t>(tiles, sms / p.C);
+  if (p.C > 1) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)p.C;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(clusters * p.C));
+    cfg.blockDim = dim3(sqk::MOE_EXPERT_THREADS);
+    cfg.dynamicSmemBytes = (size_t)kSmemBudget;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int active = 0;
+    e = max_active_clusters(down, &cfg, &active);
+    if (e != cudaSuccess) return e;
+    clusters = std::min<int64_t>(clusters, std::max(active, 1));
+  }
+  const int64_t per2 = (tiles + clusters - 1) / clusters;
+  // the sums over the ranks take the rings' place
+  p.down_pass = (int)std::min(passes(kSmemBudget - ring, cell2, per2), std::max<int64_t>(1, ring / ((int64_t)p.T * 64)));
+  p.down_ring_at = (int)((p.down_pass + sqk::MOE_WARPS - 1) * cell2);
+  return launch_dependent(down, (unsigned)(clusters * p.C), 1, sqk::MOE_EXPERT_THREADS, (size_t)(p.down_ring_at + ring), p.C, p,
+                          st);
 }
 
 template <int S, int SH>
@@ -525,8 +699,9 @@ static size_t moe_layout(sqk::MoeParams* p, char* base, int64_t T, int64_t D, in
   sqk::MoeParams q{};
   q.lists = (sqk::MoeLists*)take(sizeof(sqk::MoeLists));
   q.logits = (double*)take((size_t)(T * E) * 8);
-  q.expert = (int*)take((size_t)E * 4);
-  q.start = (int*)take((size_t)(E + 1) * 4);
+  const int64_t entries = std::min(T * k, E + T * k / sqk::MOE_ENTRY);  // every expert's last one may be short
+  q.expert = (int*)take((size_t)entries * 4);
+  q.start = (int*)take((size_t)(entries + 1) * 4);
   q.slot_token = (int*)take((size_t)(T * k) * 4);
   q.slot_weight = (float*)take((size_t)(T * k) * 4);
   q.xparts = (uint16_t*)take((size_t)(3 * T * D) * 2);
@@ -587,15 +762,15 @@ cudaError_t launch_moe_w4(const void* x, bool bf16, int64_t T, int64_t D, int64_
   p.C = 1;
   cudaError_t e;
   if (!bf16) {
-    e = launch_dependent((const void*)sqk::moe_split_kernel, (unsigned)num_sms(), 1, 0, 1, p, st);
+    e = launch_dependent((const void*)sqk::moe_split_kernel, (unsigned)num_sms(), 1, 256, 0, 1, p, st);
     if (e != cudaSuccess) return e;
   }
   if (wr) {
     const void* k = bf16 ? (wr_bf16 ? (const void*)sqk::moe_router_kernel<true, true> : (const void*)sqk::moe_router_kernel<true, false>)
                          : (wr_bf16 ? (const void*)sqk::moe_router_kernel<false, true> : (const void*)sqk::moe_router_kernel<false, false>);
-    e = launch_dependent(k, (unsigned)E, (unsigned)std::min<int64_t>(T, 8), 0, 1, p, st);
+    e = launch_dependent(k, (unsigned)E, (unsigned)std::min<int64_t>(T, 8), sqk::MOE_THREADS, 0, 1, p, st);
   } else {
-    e = launch_dependent((const void*)sqk::moe_lists_kernel, 1, 1, 0, 1, p, st);
+    e = launch_dependent((const void*)sqk::moe_lists_kernel, 1, 1, sqk::MOE_THREADS, 0, 1, p, st);
   }
   if (e != cudaSuccess) return e;
   return bf16 ? launch_experts_g<1, 2>(p, group, st) : launch_experts_g<3, 3>(p, group, st);

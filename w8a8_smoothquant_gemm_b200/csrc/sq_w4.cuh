@@ -12,6 +12,8 @@
 //     mma's packed operands want them: one shift and one three-input logic operation a pair.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "sq_ptx.cuh"
 
 namespace sqk {
@@ -21,24 +23,27 @@ constexpr int W4_BLOCK_BYTES = 64;  // bytes per block
 
 __host__ __device__ __forceinline__ int64_t w4_blocks(int64_t K) { return (K + W4_BLOCK - 1) / W4_BLOCK; }
 
-// Bits of the bf16 number 128 + v for an integer 0 <= v < 128 (exact: 128 .. 255 have spacing 1).
-__device__ __forceinline__ uint32_t bf16_128_plus(uint32_t v) { return 0x4300u + v; }
+// Codes as mma operands.  OR-ing a code into the low significand bits of 128.0 (bf16, where the
+// spacing is 1) makes 128 + code, and subtracting 128 + zero leaves code - zero, all exact: a
+// shift, a logic operation and a packed subtraction for two codes.
+__device__ __forceinline__ uint32_t w4_zero(uint32_t zero) { return zero * 0x10001u + 0x43004300u; }
 
-// Pair p of a word as two bf16 numbers (code - zero), exact; `z` holds 128 + zero twice.
-__device__ __forceinline__ uint32_t w4_pair(uint32_t word, int p, uint32_t z) {
-  uint32_t v;
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(word >> (4 * p)), "n"(0x000f000f), "n"(0x43004300));
-  uint32_t d;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(z));
-  return d;
+// The eight codes of a word as four operand pairs (code 2p - zero, code 2p + 1 - zero).
+__device__ __forceinline__ void w4_unpack(uint32_t (&a)[4], uint32_t word, uint32_t zero) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    uint32_t v;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(word >> (4 * p)), "n"(0x000f000f), "n"(0x43004300));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(a[p]) : "r"(v), "r"(zero));
+  }
 }
 
-// D += A B, 16 x 8 x 16, bf16 operands, binary32 sums.  Lane (g, t) = (lane / 4, lane % 4) holds
-// a0, a2 of row g and a1, a3 of row g + 8 for the k pairs (2t, 2t + 1) and (2t + 8, 2t + 9), b0 and
-// b1 of column g for the same k, d0, d1 of row g, columns 2t, 2t + 1, and d2, d3 of row g + 8.
-// Which k the sixteen slots stand for is free as long as A and B agree.
-__device__ __forceinline__ void mma_bf16(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
+// D += A B, 16 x 8 x 16, binary32 sums.  Lane (g, t) = (lane / 4, lane % 4) holds a0, a2 of row g
+// and a1, a3 of row g + 8 for the k pairs (2t, 2t + 1) and (2t + 8, 2t + 9), b0 and b1 of column g
+// for the same k, d0, d1 of row g, columns 2t, 2t + 1, and d2, d3 of row g + 8.  Which k the
+// sixteen slots stand for is free as long as A and B agree.
+__device__ __forceinline__ void w4_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -78,88 +83,257 @@ __device__ __forceinline__ void split_bf16_stored(float x, uint32_t part[S]) {
   split_bf16<S>(x, part);
 }
 
-// One lane's share of 16 rows x 128 codes: 16 bytes of row g and of row g + 8, and for each the
-// scale and zero point of one group of the block (lane t those of the group that holds 32 t).
-struct W4Block {
-  uint4 lo, hi;
-  uint32_t s;  // scales (bf16 bits): row g in the low half, row g + 8 in the high half
-  uint32_t z;  // zero points: row g in bits 0-7, row g + 8 in bits 8-15
-};
+// ---------------------------------------------------------------------------- the weight stream
+// A warp's share of the weights is a list of units: 16 rows x 256 codes (two blocks, 2 KB) with the
+// scales and zero points of their groups.  They travel from memory to shared memory with
+// asynchronous copies, DEPTH - 1 units ahead, in a ring that belongs to the warp alone: a lane reads
+// back only codes that it copied itself, so no barrier is needed, only the copies' own group count
+// (and a __syncwarp for the scales, which also says that the last unit's slot has been read and can
+// be filled again).  Registers hold one block, whatever the depth.
+//   What sets the depth is latency: at 6.5 TB/s and about 1 us under load an SM needs some 45 KB in
+// flight; 16 warps with two units each on their way have 64 KB.  What limits the loop once the bytes
+// are there is the unpacking (56 shifts and logic operations a block on the half-rate integer pipe,
+// about 29 clocks of an SM, against 46 in which HBM delivers a block), so everything else in it is
+// kept few: two blocks to a unit halve the control and address arithmetic.
+constexpr int W4_UNIT = 2 * W4_BLOCK;
 
-// The rows a lane reads: codes of rows g and g + 8 at this lane's 16 bytes of block 0, scales and
-// zero points of group 0, and the distance (in elements) between groups.
-struct W4Rows {
-  const char *lo, *hi;
-  const uint16_t *slo, *shi;
-  const uint8_t *zlo, *zhi;
-  int64_t pitch;
-  int last;  // last group
+__host__ __device__ __forceinline__ int w4_units(int64_t K) { return (int)((K + W4_UNIT - 1) / W4_UNIT); }
+
+struct W4Base {  // bases that a whole CTA shares, so that offsets are 32-bit
+  const char* codes;
+  const uint16_t* scales;
+  const uint8_t* zeros;
+  uint32_t row_bytes;  // of a row of codes
+  uint32_t pitch;      // scales of a group
+  int groups;          // groups of a row
 };
 
 template <int GW, bool ASYM>
-__device__ __forceinline__ void w4_load(W4Block& w, const W4Rows& r, int64_t b, int t) {
-  w.lo = ldg_stream16(r.lo + b * W4_BLOCK_BYTES);
-  w.hi = ldg_stream16(r.hi + b * W4_BLOCK_BYTES);
-  // the padding of the last block has no group of its own: any finite scale will do there
-  const int64_t g = min((int)(b * (4 / GW)) + t / GW, r.last) * r.pitch;
-  w.s = (uint32_t)__ldg(r.slo + g) | ((uint32_t)__ldg(r.shi + g) << 16);
-  if (ASYM) w.z = (uint32_t)__ldg(r.zlo + g) | ((uint32_t)__ldg(r.zhi + g) << 8);
+struct W4Slot {  // of the ring: per block, codes of rows g and of rows g + 8; then scales, zero points
+  static constexpr int GPB = 4 / GW, GPU = 2 * GPB;  // groups per block, per unit
+  static constexpr int SCALES = 2048, ZEROS = SCALES + GPU * 32, BYTES = ZEROS + (ASYM ? GPU * 16 : 0);
+};
+
+// 16 bytes, or zeros where `bytes` is 0.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes = 16) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async16_if(bool on, uint32_t dst, const void* src) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(dst),
+               "l"(src), "r"((uint32_t)on)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async8_if(bool on, uint32_t dst, const void* src) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p cp.async.ca.shared.global [%0], [%1], 8;\n\t}" ::"r"(dst),
+               "l"(src), "r"((uint32_t)on)
+               : "memory");
+}
+// Loads from shared memory by address.  Volatile: they keep their place between the waits.
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t at, uint16_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(v) : "memory");
+}
+__device__ __forceinline__ void sts8(uint32_t at, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// acc += scale * ((codes - zero) . x) for one block: NT column tiles of 8, S bf16 parts of x, GW
-// 32-code words per scale.  xload(nt, s, w) gives the 8 values of x at 32 w + 8 t of column
-// 8 nt + g, part s.  The integer part is summed by the tensor cores in binary32 over one group
-// (codes - zero and x are exact bf16, their products exact), then scaled and added in binary32.
-template <int NT, int S, int GW, bool ASYM, typename XLoad>
-__device__ __forceinline__ void w4_mac(float (&acc)[NT][4], const W4Block& w, int lane, XLoad xload) {
-  const uint32_t* lo = &w.lo.x;
-  const uint32_t* hi = &w.hi.x;
-  float tmp[NT][4];
-  uint32_t zlo = bf16_128_plus(8) * 0x10001u, zhi = zlo;
-  float slo, shi;
+// What a lane copies of the next unit.
+struct W4Cursor {
+  const char *lo, *hi;  // its 16 bytes of rows g and g + 8
+  uint32_t sc;          // element offset of the scales it copies
+  uint32_t sc_end;      // and of those of the last group: the padding of a row's last block has no
+                        // group of its own, and any finite scale will do there
+};
+
+// At unit u of the tile whose rows are row0 .. row0 + 7 and row8 .. row8 + 7 (relative to the base);
+// rows past last_row repeat it.  ALIGNED: 8 rows' scales (zero points) are one 16-byte (8-byte) piece.
+template <int GW, bool ASYM, bool ALIGNED>
+__device__ __forceinline__ W4Cursor w4_place(const W4Base& base, uint32_t row0, uint32_t row8, uint32_t last_row, int u,
+                                             int lane) {
+  const uint32_t col = (uint32_t)u * (2 * W4_BLOCK_BYTES) + (lane % 4) * 16;
+  W4Cursor c;
+  c.lo = base.codes + (min(row0 + lane / 4, last_row) * base.row_bytes + col);
+  c.hi = base.codes + (min(row8 + lane / 4, last_row) * base.row_bytes + col);
+  // lane 2 q + h copies half h of group q (the last 8 rows stand in for a half that is past the
+  // end); where that is no aligned piece, lane r < 16 fetches row r of every group
+  uint32_t row, group = (uint32_t)u * W4Slot<GW, ASYM>::GPU;
+  if (ALIGNED) {
+    row = min(lane % 2 ? row8 : row0, last_row - 7);
+    group += lane / 2;
+  } else {
+    row = min(lane < 8 ? row0 + lane : row8 + lane % 8, last_row);
+  }
+  c.sc = group * base.pitch + row;
+  c.sc_end = (uint32_t)(base.groups - 1) * base.pitch + row;
+  return c;
+}
+
+// Starts the copies of the cursor's unit, of which only the first block exists where `half`.
+template <int GW, bool ASYM, bool ALIGNED>
+__device__ __forceinline__ void w4_issue(uint32_t slot, const W4Base& base, W4Cursor& c, bool half, int lane) {
+  using L = W4Slot<GW, ASYM>;
+  const uint32_t second = half ? 0u : 16u;
+  cp_async16(slot + lane * 16, c.lo);
+  cp_async16(slot + 512 + lane * 16, c.hi);
+  cp_async16(slot + 1024 + lane * 16, c.lo + W4_BLOCK_BYTES, second);
+  cp_async16(slot + 1536 + lane * 16, c.hi + W4_BLOCK_BYTES, second);
+  if (ALIGNED) {
+    const uint32_t at = min(c.sc, c.sc_end);
+    cp_async16_if(lane < 2 * L::GPU, slot + L::SCALES + lane * 16, base.scales + at);
+    if (ASYM) cp_async8_if(lane < 2 * L::GPU, slot + L::ZEROS + lane * 8, base.zeros + at);
+  } else if (lane < 16) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i % GW == 0) {
-      uint32_t s = w.s, z = w.z;
-      if (GW < 4) {  // the lane of this quad that loaded the group of word i
-        s = __shfl_sync(0xffffffffu, w.s, (lane & ~3) | i);
-        if (ASYM) z = __shfl_sync(0xffffffffu, w.z, (lane & ~3) | i);
-      }
-      slo = bf16lo(s);
-      shi = bf16hi(s);
-      if (ASYM) {
-        zlo = bf16_128_plus(z & 0xffu) * 0x10001u;
-        zhi = bf16_128_plus((z >> 8) & 0xffu) * 0x10001u;
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) tmp[n][0] = tmp[n][1] = tmp[n][2] = tmp[n][3] = 0.0f;
+    for (int q = 0; q < L::GPU; ++q) {
+      const uint32_t at = min(c.sc + q * base.pitch, c.sc_end);
+      sts16(slot + L::SCALES + q * 32 + lane * 2, __ldg(base.scales + at));
+      if (ASYM) sts8(slot + L::ZEROS + q * 16 + lane, __ldg(base.zeros + at));
     }
-    uint32_t a[4], c[4];
+  }
+  c.lo += 2 * W4_BLOCK_BYTES;
+  c.hi += 2 * W4_BLOCK_BYTES;
+  c.sc += L::GPU * base.pitch;
+}
+
+// acc += scale * ((codes - zero) . x) for the unit in `slot`: NT column tiles of 8, S parts of x.
+// xload(nt, s, w) gives the 8 values of x at 32 w + 8 t (w < 8) of column 8 nt + g, part s.  The
+// integer part is summed by the tensor cores in binary32 over one group (codes - zero and x are
+// exact operands, their products exact), then scaled and added in binary32.
+template <int NT, int S, int GW, bool ASYM, int NTA, typename XLoad>
+__device__ __forceinline__ void w4_mac(float (&acc)[NTA][4], uint32_t slot, int lane, XLoad xload) {
+  static_assert(NT <= NTA, "column tiles beyond the sums");
+  using L = W4Slot<GW, ASYM>;
+  const uint32_t row = lane / 4;
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      a[p] = w4_pair(lo[i], p, zlo);
-      c[p] = w4_pair(hi[i], p, zhi);
-    }
+  for (int b = 0; b < 2; ++b) {
+    const uint4 wl = lds128(slot + b * 1024 + lane * 16), wh = lds128(slot + b * 1024 + 512 + lane * 16);
+    const uint32_t lo[4] = {wl.x, wl.y, wl.z, wl.w}, hi[4] = {wh.x, wh.y, wh.z, wh.w};
+    float tmp[NT][4];
+    uint32_t zlo = w4_zero(8), zhi = zlo;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int i = 0; i < 4; ++i) {
+      const int q = b * L::GPB + i / GW;  // group within the unit
+      if (i % GW == 0) {
+        if (ASYM) {
+          zlo = w4_zero(lds8(slot + L::ZEROS + q * 16 + row));
+          zhi = w4_zero(lds8(slot + L::ZEROS + q * 16 + 8 + row));
+        }
 #pragma unroll
-      for (int s = 0; s < S; ++s) {
-        const uint4 x = xload(n, s, i);
-        mma_bf16(tmp[n], a[0], c[0], a[1], c[1], x.x, x.y);
-        mma_bf16(tmp[n], a[2], c[2], a[3], c[3], x.z, x.w);
+        for (int n = 0; n < NT; ++n) tmp[n][0] = tmp[n][1] = tmp[n][2] = tmp[n][3] = 0.0f;
       }
-    }
-    if (i % GW == GW - 1) {
+      uint32_t a[4], c[4];
+      w4_unpack(a, lo[i], zlo);
+      w4_unpack(c, hi[i], zhi);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        acc[n][0] = __fmaf_rn(slo, tmp[n][0], acc[n][0]);
-        acc[n][1] = __fmaf_rn(slo, tmp[n][1], acc[n][1]);
-        acc[n][2] = __fmaf_rn(shi, tmp[n][2], acc[n][2]);
-        acc[n][3] = __fmaf_rn(shi, tmp[n][3], acc[n][3]);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          const uint4 x = xload(n, s, 4 * b + i);
+          w4_mma(tmp[n], a[0], c[0], a[1], c[1], x.x, x.y);
+          w4_mma(tmp[n], a[2], c[2], a[3], c[3], x.z, x.w);
+        }
+      }
+      if (i % GW == GW - 1) {
+        const float slo = bf16lo(lds16(slot + L::SCALES + q * 32 + row * 2));
+        const float shi = bf16lo(lds16(slot + L::SCALES + q * 32 + 16 + row * 2));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          acc[n][0] = __fmaf_rn(slo, tmp[n][0], acc[n][0]);
+          acc[n][1] = __fmaf_rn(slo, tmp[n][1], acc[n][1]);
+          acc[n][2] = __fmaf_rn(shi, tmp[n][2], acc[n][2]);
+          acc[n][3] = __fmaf_rn(shi, tmp[n][3], acc[n][3]);
+        }
       }
     }
   }
 }
+
+// ---------------------------------------------------------------------------- runs and cells
+// A CTA's line of units (tile after tile) is cut into equal runs, one a warp.  A warp's sum over its
+// part of a tile goes to a cell of its own; the cells of a tile are then added in the order of the
+// warps.  Cells lie in the order of the line, so there is at most one more per run than tiles.
+constexpr int W4_RP = 20;  // floats between a cell's tokens: 16 rows, padded to spread the banks
+
+template <int WARPS>
+struct W4Runs {  // in shared memory
+  int first_cell[WARPS], first_tile[WARPS];
+};
+
+// n / d for n < 2^27 with inv = 1 / d: the quotient in binary32 is off by less than one.
+__device__ __forceinline__ int w4_div(int n, int d, float inv) {
+  const int q = (int)__fmul_rn((float)n, inv), r = n - q * d;
+  return q + (r >= d) - (r < 0);
+}
+
+// Where run w of a line begins.
+template <int WARPS>
+__device__ __forceinline__ int w4_cut(int line, int w) {
+  return (int)((uint32_t)(line * w) / (uint32_t)WARPS);
+}
+
+struct W4Run {  // this warp's
+  int units;    // of the line
+  int tile, b;  // where it begins
+  int cell;     // its first cell
+};
+
+// Fills `runs` (warp 0; a __syncthreads must follow before it is read) and returns this warp's run.
+template <int WARPS>
+__device__ __forceinline__ W4Run w4_runs(W4Runs<WARPS>& runs, int line, int per_tile, int warp, int lane) {
+  static_assert(WARPS <= 32, "a lane per run");
+  const float inv = __frcp_rn((float)per_tile);
+  const int a0 = w4_cut<WARPS>(line, lane), a1 = lane < WARPS ? w4_cut<WARPS>(line, lane + 1) : a0;
+  const int at = w4_div(a0, per_tile, inv), n = a1 > a0 ? w4_div(a1 - 1, per_tile, inv) - at + 1 : 0;
+  int sum = n;
+#pragma unroll
+  for (int o = 1; o < WARPS; o *= 2) {
+    const int other = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += other;
+  }
+  if (warp == 0 && lane < WARPS) {
+    runs.first_cell[lane] = sum - n;
+    runs.first_tile[lane] = at;
+  }
+  W4Run r;
+  r.units = __shfl_sync(0xffffffffu, a1 - a0, warp);
+  r.tile = __shfl_sync(0xffffffffu, at, warp);
+  r.b = __shfl_sync(0xffffffffu, a0 - at * per_tile, warp);
+  r.cell = __shfl_sync(0xffffffffu, sum - n, warp);
+  return r;
+}
+
+// Calls add(cell) for the cells of tile `ti`, in order; inv = 1 / line.
+template <int WARPS, typename Add>
+__device__ __forceinline__ void w4_cells_of(const W4Runs<WARPS>& runs, int ti, int line, float inv, int per_tile,
+                                            Add add) {
+  const int w0 = w4_div(WARPS * (ti * per_tile + 1) - 1, line, inv);
+  const int w1 = w4_div(WARPS * (ti + 1) * per_tile - 1, line, inv);
+#pragma unroll 1
+  for (int w = w0; w <= w1; ++w)
+    if (w4_cut<WARPS>(line, w) != w4_cut<WARPS>(line, w + 1))  // else an empty run
+      add(runs.first_cell[w] + ti - runs.first_tile[w]);
+}
+
+// part i of n equal parts of a count whose quotient and remainder by n are q and r: where it begins
+__device__ __forceinline__ int64_t w4_part(int64_t i, int64_t q, int r) { return i * q + min(i, (int64_t)r); }
 
 // Lets the previous kernel of a programmatic launch finish before anything it wrote is read.  What
 // that kernel may have written (activations, workspaces) is then read with plain loads: the

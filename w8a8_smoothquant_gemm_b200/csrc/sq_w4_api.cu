@@ -105,6 +105,7 @@ sq_status run_moe(const MoeArgs& a, bool routed, void* stream) {
   if (st != SQ_OK) return st;
   st = check_packed(a.w2, a.s2);
   if (st != SQ_OK) return st;
+  if (!aligned(a.s13, 16) || !aligned(a.s2, 16) || !aligned(a.z13, 16) || !aligned(a.z2, 16)) return SQ_ERR_ALIGNMENT;
   if (a.D % 16 != 0 || a.F % 16 != 0 || !aligned(a.y, elt_size(a.ydt))) return SQ_ERR_ALIGNMENT;
   if (!aligned(a.wr, 16) || !aligned(a.ids, 4) || !aligned(a.wts, 4) || !aligned(a.ids_in, 4) || !aligned(a.wts_in, 4))
     return SQ_ERR_ALIGNMENT;
@@ -173,7 +174,9 @@ sq_status sq_w4_gemm(const void* x, sq_dtype dt, int64_t M, int64_t K, int64_t l
   st = check_packed(Wq, scales);
   if (st != SQ_OK) return st;
   if (K % 16 != 0 || !aligned(y, elt_size(ydt))) return SQ_ERR_ALIGNMENT;
-  if (K > SQ_MAX_K || N > (int64_t)INT_MAX / 2 || M > SQ_W4_MAX_M) return SQ_ERR_UNSUPPORTED;
+  if (K > SQ_MAX_K || N > (int64_t)INT_MAX || M > SQ_W4_MAX_M) return SQ_ERR_UNSUPPORTED;
+  if ((K + group - 1) / group * N > (int64_t)UINT_MAX) return SQ_ERR_UNSUPPORTED;  // 32-bit offsets of scales,
+  if (sq_w4_row_bytes(K) > (1ll << 35) / N) return SQ_ERR_UNSUPPORTED;  // and of one block's codes
   return cuda_status(sqh::launch_w4_gemm(x, dt == SQ_BF16, M, K, ldx, Wq, scales, zeros, N, group, y, ydt == SQ_BF16,
                                          ldy, static_cast<cudaStream_t>(stream)));
 }

@@ -9,164 +9,202 @@
 // step consumes 256 weights, so the tensor pipe is far from its limit (tcgen05 would want the
 // unpacked operand written to shared memory first, four times the bytes of the codes).
 //
-// A CTA owns 16 WR rows of weights over its K range; its 8 warps are WR row tiles x 8 / WR K
-// slices (interleaved blocks, so a CTA reads whole lines).  x is staged in shared memory once as
-// bf16 parts (one for bf16, three for binary32, which together are x exactly).  Partial sums meet
-// in shared memory and, when K is cut over a cluster because there are few row tiles, in
-// distributed shared memory, always in the same order: no atomics, no workspace.
+// One CTA per SM (or cluster of CTAs, which then cut K between them because there are few rows or
+// x is long) owns a run of 16-row tiles.  Its (tile, block) list is cut into 16 equal runs, one a
+// warp, whatever the sizes; a warp streams its run through its ring without a pause (sq_w4.cuh).
+// x is staged in shared memory once, as bf16 parts (one for bf16, three for binary32, which together
+// are x exactly); where it does not fit it comes in chunks of K.  A warp's sum over its part of a
+// tile goes to a cell of its own, and the cells of a tile are added in order at the end (and over
+// the cluster through distributed shared memory): no atomics, no workspace.
 #include <algorithm>
 
 #include "sq_w4.cuh"
 
 namespace sqk {
 
-constexpr int W4G_THREADS = 256;
-constexpr int W4G_DEPTH = 4;  // blocks a warp keeps in flight
+constexpr int W4G_WARPS = 16;  // of a CTA
+constexpr int W4G_DEPTH = 3;   // slots of a warp's ring
 
 struct W4GemmParams {
   const char* x;
   int64_t ldx_bytes;
   int M, K;
-  const char* wq;
-  const uint16_t* sg;
-  const uint8_t* zp;
-  int64_t N, row_bytes;
-  int groups;
+  W4Base w;
+  int64_t N;
   void* y;
   int64_t ldy;
   int y_bf16;
-  int C;      // CTAs of the cluster, over K
-  int chunk;  // blocks of x staged at a time
+  int C;         // CTAs of a cluster, over K
+  int clusters;  // of the grid, over the tiles
+  int units;     // of K
+  bool odd;      // the last one has one block
+  int tile_q, tile_r;    // tiles / clusters and the remainder: the first tile_r clusters have one more
+  int unit_q, unit_r;    // the same for the units of K over the ranks
+  int chunk;     // units of x staged at a time
+  int pass;      // tiles whose partial sums fit
+  int out_at, cell_at, ring_at;  // shared memory: x, then sums over chunks or ranks, cells, rings (sums
+                                 // that no chunk adds to take the rings' place when those are empty)
 };
 
-template <int NT, int S, int GW, bool ASYM, int WR>
-__global__ void __launch_bounds__(W4G_THREADS) w4_gemm_kernel(const W4GemmParams p) {
-  constexpr int WK = 8 / WR, ROWS = 16 * WR, RP = ROWS + 4;  // RP: padded row count, conflict-free partial sums
+template <int NT, int S, int GW, bool ASYM, bool ALIGNED>
+__global__ void __launch_bounds__(32 * W4G_WARPS, 1) w4_gemm_kernel(const W4GemmParams p) {
+  constexpr int WARPS = W4G_WARPS, THREADS = 32 * WARPS, DEPTH = W4G_DEPTH, SLOT = W4Slot<GW, ASYM>::BYTES, RP = W4_RP;
   extern __shared__ __align__(16) char smem[];
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
-  const int wr = warp % WR, wk = warp / WR;
-  const int rank = blockIdx.x % p.C;
-  const int64_t row0 = (int64_t)(blockIdx.x / p.C) * ROWS;
+  __shared__ W4Runs<WARPS> runs;
+  const int tid = threadIdx.x, lane = tid % 32, g = lane / 4, t = lane % 4;
+  const int warp = __shfl_sync(0xffffffffu, tid / 32, 0);  // the same in every lane, and known to be
+  const int rank = blockIdx.x % p.C, cluster = blockIdx.x / p.C;
   const int m0 = blockIdx.y * 8 * NT, Mr = min(8 * NT, p.M - m0);
-  const int nb = (int)w4_blocks(p.K);
-  const int b0 = (int)((int64_t)nb * rank / p.C), b1 = (int)((int64_t)nb * (rank + 1) / p.C);
+  const int b0 = (int)w4_part(rank, p.unit_q, p.unit_r), b1 = b0 + p.unit_q + (rank < p.unit_r);
+  const int64_t t0 = w4_part(cluster, p.tile_q, p.tile_r);
+  const int my_tiles = p.tile_q + (cluster < p.tile_r);
+  const uint32_t last_row = (uint32_t)min(p.N - 1 - t0 * 16, (int64_t)my_tiles * 16 - 1);
+  float* out = reinterpret_cast<float*>(smem + p.out_at);     // [tile of the pass][token][row]
+  float* cells = reinterpret_cast<float*>(smem + p.cell_at);  // [cell][token][row], padded
+  const uint32_t ring = smem_u32(smem + p.ring_at) + warp * DEPTH * SLOT;
+  W4Base base = p.w;
+  base.codes += t0 * 16 * base.row_bytes;
+  base.scales += t0 * 16;
+  if (ASYM) base.zeros += t0 * 16;
 
   wait_for_previous_kernel();
   allow_dependent_launch();
 
-  W4Rows r;
-  {
-    const int64_t last = p.N - 1;  // rows past the end repeat the last one and are not stored
-    const int64_t lo = min(row0 + wr * 16 + g, last), hi = min(row0 + wr * 16 + g + 8, last);
-    r.lo = p.wq + lo * p.row_bytes + t * 16;
-    r.hi = p.wq + hi * p.row_bytes + t * 16;
-    r.slo = p.sg + lo;
-    r.shi = p.sg + hi;
-    r.zlo = p.zp + (ASYM ? lo : 0);
-    r.zhi = p.zp + (ASYM ? hi : 0);
-    r.pitch = p.N;
-    r.last = p.groups - 1;
-  }
+  const int pitch = p.chunk * (2 * W4_UNIT) + 64;  // bytes per staged token: rows 64 bytes apart modulo 128
+  uint32_t xs[NT];                       // this lane's columns (addresses); absent tokens read the last one
+#pragma unroll
+  for (int n = 0; n < NT; ++n) xs[n] = smem_u32(smem) + min(8 * n + g, Mr - 1) * pitch + t * 16;
+  const int plane = Mr * pitch;
+  const bool whole = p.chunk >= b1 - b0;
 
-  float acc[NT][4];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-
-  const int pitch = p.chunk * 256 + 64;  // bytes per staged token: rows 64 bytes apart modulo 128
-  const char* xs[NT];                    // this lane's columns; absent tokens read the last one
-#pragma unroll
-  for (int n = 0; n < NT; ++n) xs[n] = smem + (int64_t)min(8 * n + g, Mr - 1) * pitch + t * 16;
-  const int64_t plane = (int64_t)Mr * pitch;
-
-  for (int c0 = b0; c0 < b1; c0 += p.chunk) {
-    const int c1 = min(c0 + p.chunk, b1);
-    W4Block w[W4G_DEPTH];
-#pragma unroll
-    for (int u = 0; u < W4G_DEPTH; ++u) {
-      const int b = c0 + wk + u * WK;
-      if (b < c1) w4_load<GW, ASYM>(w[u], r, b, t);
-    }
-    if (c0 != b0) __syncthreads();  // the last chunk has been read
-    const int vecs = (c1 - c0) * 16;  // 8-value pieces per token
-    for (int i = tid; i < vecs * Mr; i += W4G_THREADS) {
-      const int m = i / vecs, v = i % vecs;
-      const int64_t k = (int64_t)c0 * W4_BLOCK + v * 8;
-      char* dst = smem + (int64_t)m * pitch + v * 16;
-      const char* src = p.x + (m0 + m) * p.ldx_bytes;
-      if (S == 1) {
-        uint4 a = make_uint4(0, 0, 0, 0);
-        if (k < p.K) a = *reinterpret_cast<const uint4*>(src + k * 2);
-        *reinterpret_cast<uint4*>(dst) = a;
-      } else {
-        float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (k < p.K) {
-          *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(src + k * 4);
-          *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(src + k * 4 + 16);
-        }
-        uint32_t part[8][S];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) split_bf16<S>(f[e], part[e]);
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-          *reinterpret_cast<uint4*>(dst + s * plane) =
-              make_uint4(part[0][s] | (part[1][s] << 16), part[2][s] | (part[3][s] << 16),
-                         part[4][s] | (part[5][s] << 16), part[6][s] | (part[7][s] << 16));
-      }
-    }
-    __syncthreads();
-    for (int bb = c0 + wk; bb < c1; bb += WK * W4G_DEPTH) {
-#pragma unroll
-      for (int u = 0; u < W4G_DEPTH; ++u) {
-        const int b = bb + u * WK;
-        if (b < c1) {
-          w4_mac<NT, S, GW, ASYM>(acc, w[u], lane, [&](int n, int s, int i) {
-            return *reinterpret_cast<const uint4*>(xs[n] + s * plane + (b - c0) * 256 + i * 64);
-          });
-          const int next = b + WK * W4G_DEPTH;
-          if (next < c1) w4_load<GW, ASYM>(w[u], r, next, t);
+  for (int p0 = 0; p0 < my_tiles; p0 += p.pass) {
+    const int n_tiles = min(p.pass, my_tiles - p0);
+    for (int c0 = b0; c0 < b1; c0 += p.chunk) {
+      const int units = min(p.chunk, b1 - c0), line = n_tiles * units;
+      if (c0 != b0 || p0 != 0) __syncthreads();  // x, the cells and the sums of the last turn have been read
+      const bool stage = !whole || p0 == 0;
+      const int vecs = units * (W4_UNIT / 8);  // 8-value pieces per token
+      if (S == 1 && stage) {
+        for (int m = 0; m < Mr; ++m) {
+          const char* src = p.x + (m0 + m) * p.ldx_bytes + (int64_t)c0 * W4_UNIT * 2;
+          for (int v = tid; v < vecs; v += THREADS) {
+            if (c0 * W4_UNIT + v * 8 < p.K) cp_async16(smem_u32(smem + m * pitch + v * 16), src + v * 16);
+            else *reinterpret_cast<uint4*>(smem + m * pitch + v * 16) = make_uint4(0, 0, 0, 0);
+          }
         }
       }
-    }
-  }
+      cp_commit();
+      {
+        const W4Run run = w4_runs<WARPS>(runs, line, units, warp, lane);
+        int b = run.b, left = run.units;
+        float* cell = cells + run.cell * Mr * RP + g;
 
-  // partial sums: red[wk][token][row]
-  __syncthreads();
-  float* red = reinterpret_cast<float*>(smem);
+        int to_load = left, load_tile = run.tile, load_b = units - b;
+        W4Cursor cur = w4_place<GW, ASYM, ALIGNED>(base, (p0 + load_tile) * 16, (p0 + load_tile) * 16 + 8, last_row, c0 + b, lane);
+        const bool odd = p.odd && c0 + units == p.units;  // the last unit of a row is half a one
+        auto issue = [&](uint32_t into) {
+          if (to_load > 0) {
+            w4_issue<GW, ASYM, ALIGNED>(into, base, cur, odd && load_b == 1, lane);
+            --to_load;
+            if (--load_b == 0) {
+              load_b = units;
+              ++load_tile;
+              const uint32_t row = (p0 + load_tile) * 16;
+              cur = w4_place<GW, ASYM, ALIGNED>(base, row, row + 8, last_row, c0, lane);
+            }
+          }
+          cp_commit();
+        };
+#pragma unroll 1
+        for (int u = 0; u < DEPTH - 1; ++u) issue(ring + u * SLOT);
+        if (S > 1 && stage) {
+          for (int m = 0; m < Mr; ++m) {
+            const char* src = p.x + (m0 + m) * p.ldx_bytes + (int64_t)c0 * W4_UNIT * 4;
+            for (int v2 = tid; v2 < vecs; v2 += THREADS) {
+              float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+              if (c0 * W4_UNIT + v2 * 8 < p.K) {
+                *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(src + v2 * 32);
+                *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(src + v2 * 32 + 16);
+              }
+              uint32_t part[8][S];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    float* q = red + (wk * 8 * NT + 8 * n + 2 * t) * RP + wr * 16 + g;
-    q[0] = acc[n][0];
-    q[RP] = acc[n][1];
-    q[8] = acc[n][2];
-    q[RP + 8] = acc[n][3];
-  }
-  __syncthreads();
-  const int outs = Mr * ROWS;
-  if (p.C == 1) {
-    for (int o = tid; o < outs; o += W4G_THREADS) {
-      const int m = o / ROWS, row = o % ROWS;
-      float v = red[m * RP + row];
+              for (int e = 0; e < 8; ++e) split_bf16<S>(f[e], part[e]);
 #pragma unroll
-      for (int k = 1; k < WK; ++k) v = __fadd_rn(v, red[(k * 8 * NT + m) * RP + row]);
-      if (row0 + row < p.N) store_out(p.y, (m0 + m) * p.ldy + row0 + row, v, p.y_bf16);
+              for (int s = 0; s < S; ++s)
+                *reinterpret_cast<uint4*>(smem + m * pitch + v2 * 16 + s * plane) =
+                    make_uint4(part[0][s] | (part[1][s] << 16), part[2][s] | (part[3][s] << 16),
+                               part[4][s] | (part[5][s] << 16), part[6][s] | (part[7][s] << 16));
+            }
+          }
+        }
+        cp_wait<DEPTH - 1>();  // x; the ring's blocks are younger
+        __syncthreads();
+
+        float acc[NT][4];
+#pragma unroll
+        for (int k = 0; k < NT; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.0f;
+        uint32_t slot = ring, spent = ring + (DEPTH - 1) * SLOT;  // the next block's, the last one's
+        uint32_t xo = b * (2 * W4_UNIT);
+        while (left > 0) {
+          const int part = min(left, units - b);  // of the tile
+          left -= part;
+#pragma unroll 1
+          for (int i = 0; i < part; ++i) {
+            cp_wait<DEPTH - 2>();
+            __syncwarp();
+            issue(spent);
+            w4_mac<NT, S, GW, ASYM>(acc, slot, lane,
+                                    [&](int k, int s, int w) { return lds128(xs[k] + xo + s * plane + w * 64); });
+            spent = slot;
+            slot = slot == ring + (DEPTH - 1) * SLOT ? ring : slot + SLOT;
+            xo += 2 * W4_UNIT;
+          }
+          {  // the end of this warp's part of the tile
+#pragma unroll
+            for (int k = 0; k < NT; ++k) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const int m = 8 * k + 2 * t + c;
+                if (m < Mr) {
+                  cell[m * RP] = acc[k][c];
+                  cell[m * RP + 8] = acc[k][2 + c];
+                }
+                acc[k][c] = acc[k][2 + c] = 0.0f;
+              }
+            }
+            cell += Mr * RP;
+            b = 0;
+            xo = 0;
+          }
+        }
+      }
+      __syncthreads();
+      const int outs = n_tiles * Mr * 16;
+      const float inv_line = __frcp_rn((float)line);
+      const bool last = c0 + p.chunk >= b1;
+      for (int o = tid; o < outs; o += THREADS) {
+        const int row = o % 16, mt = o / 16, ti = mt / Mr, m = mt - ti * Mr;
+        const float* q = cells + m * RP + row;
+        float v = c0 == b0 ? 0.0f : out[o];
+        w4_cells_of<WARPS>(runs, ti, line, inv_line, units, [&](int c) { v = __fadd_rn(v, q[c * Mr * RP]); });
+        const int64_t n = (t0 + p0 + ti) * 16 + row;
+        if (p.C > 1 || !last) out[o] = v;
+        else if (n < p.N) store_out(p.y, (m0 + m) * p.ldy + n, v, p.y_bf16);
+      }
     }
-    return;
+    if (p.C > 1) {
+      cluster_sync();
+      const int outs = n_tiles * Mr * 16;
+      for (int o = rank * THREADS + tid; o < outs; o += p.C * THREADS) {
+        const int row = o % 16, mt = o / 16, ti = mt / Mr, m = mt - ti * Mr;
+        float v = ld_dsmem_f32(out + o, 0);
+        for (int c = 1; c < p.C; ++c) v = __fadd_rn(v, ld_dsmem_f32(out + o, c));
+        const int64_t n = (t0 + p0 + ti) * 16 + row;
+        if (n < p.N) store_out(p.y, (m0 + m) * p.ldy + n, v, p.y_bf16);
+      }
+      cluster_sync();  // no CTA leaves, or reuses its sums, while they are read
+    }
   }
-  for (int o = tid; o < outs; o += W4G_THREADS) {  // each thread sums its own cells, in place
-    const int m = o / ROWS, row = o % ROWS;
-    float v = red[m * RP + row];
-#pragma unroll
-    for (int k = 1; k < WK; ++k) v = __fadd_rn(v, red[(k * 8 * NT + m) * RP + row]);
-    red[m * RP + row] = v;
-  }
-  cluster_sync();
-  for (int o = rank * W4G_THREADS + tid; o < outs; o += p.C * W4G_THREADS) {
-    const int m = o / ROWS, row = o % ROWS;
-    float v = ld_dsmem_f32(red + m * RP + row, 0);
-    for (int c = 1; c < p.C; ++c) v = __fadd_rn(v, ld_dsmem_f32(red + m * RP + row, c));
-    if (row0 + row < p.N) store_out(p.y, (m0 + m) * p.ldy + row0 + row, v, p.y_bf16);
-  }
-  cluster_sync();  // no CTA leaves while its sums are read
 }
 
 }  // namespace sqk
@@ -174,57 +212,115 @@ __global__ void __launch_bounds__(W4G_THREADS) w4_gemm_kernel(const W4GemmParams
 namespace sqh {
 namespace {
 
-constexpr int kSmemBudget = 200 * 1024;
+constexpr int64_t kSmemBudget = 226 * 1024;  // of 227 KB; the rest covers the static arrays
 
-template <int NT, int S, int GW, bool ASYM, int WR>
-cudaError_t launch_w4_gemm_t(sqk::W4GemmParams p, cudaStream_t st) {
-  const int rows = 16 * WR, wk = 8 / WR;
-  const int64_t tiles = (p.N + rows - 1) / rows, mt = (p.M + 8 * NT - 1) / (8 * NT);
-  const int nb = (int)sqk::w4_blocks(p.K);
-  int C = 1;
-  while (C < 8 && tiles * mt * C < 2 * num_sms() && nb / (2 * C) >= wk) C *= 2;
-  const int mr = std::min(p.M, 8 * NT);
-  const int64_t per_block = (int64_t)S * mr * 256, fixed = (int64_t)S * mr * 64;
-  p.C = C;
-  p.chunk = (int)std::max<int64_t>(1, std::min<int64_t>((nb + C - 1) / C, (kSmemBudget - fixed) / per_block));
-  const int64_t red = (int64_t)wk * 8 * NT * (rows + 4) * 4;
-  const size_t smem = (size_t)std::max(fixed + p.chunk * per_block, red);
-  auto kern = sqk::w4_gemm_kernel<NT, S, GW, ASYM, WR>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget);
+// Cells of a pass of n tiles of `units` units: one for each tile that a warp's run touches.
+int64_t w4_cells(int64_t n, int64_t units, int warps) {
+  const int64_t line = n * units;
+  int64_t c = 0;
+  for (int w = 0; w < warps; ++w) {
+    const int64_t a0 = line * w / warps, a1 = line * (w + 1) / warps;
+    if (a1 > a0) c += (a1 - 1) / units - a0 / units + 1;
+  }
+  return c;
+}
+
+// Launches if x and the sums fit in shared memory whole, or if `chunks` allows pieces; *fits says.
+template <int NT, int S, int GW, bool ASYM, bool ALIGNED>
+cudaError_t launch_w4_gemm_t(sqk::W4GemmParams p, bool chunks, bool* fits, cudaStream_t st) {
+  constexpr int WARPS = sqk::W4G_WARPS;
+  auto kern = sqk::w4_gemm_kernel<NT, S, GW, ASYM, ALIGNED>;
+  const int64_t tiles = (p.N + 15) / 16, mt = (p.M + 8 * NT - 1) / (8 * NT);
+  const int nu = sqk::w4_units(p.K), mr = std::min(p.M, 8 * NT);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBudget);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(tiles * C), (unsigned)mt);
-  cfg.blockDim = dim3(sqk::W4G_THREADS);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(32 * WARPS);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)C;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = C > 1 ? 2 : 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  const int64_t ring = (int64_t)WARPS * sqk::W4G_DEPTH * sqk::W4Slot<GW, ASYM>::BYTES;
+  const int64_t cell = (int64_t)mr * sqk::W4_RP * 4, out = (int64_t)mr * 16 * 4;  // bytes per cell, per tile
+  const int64_t x_unit = (int64_t)S * mr * (2 * sqk::W4_UNIT), x_fixed = (int64_t)S * mr * 64;
+  // The cluster: as few CTAs as hold x and the sums of their tiles whole, or, with few tiles, as many
+  // as still give every CTA an SM; each keeps at least two units of a tile.
+  const int sms = (int)std::max<int64_t>(1, num_sms() / mt);
+  int64_t used = 0;
+  for (int C = 1;; C *= 2) {
+    const int64_t units = (nu + C - 1) / C;
+    const bool more = C < 8 && units >= 4;
+    p.C = C;
+    p.clusters = (int)std::min<int64_t>(tiles, std::max(sms / C, 1));
+    if (C > 1) {
+      attr[0].val.clusterDim.x = (unsigned)C;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      cfg.gridDim = dim3((unsigned)(p.clusters * C), 1);
+      cfg.dynamicSmemBytes = (size_t)kSmemBudget;
+      int active = 0;
+      e = max_active_clusters((const void*)kern, &cfg, &active);
+      if (e != cudaSuccess) return e;
+      p.clusters = (int)std::min<int64_t>(p.clusters, std::max<int64_t>(1, active / mt));
+    }
+    const int64_t per = (tiles + p.clusters - 1) / p.clusters;
+    int64_t n_cells = 0;  // CTAs have per or per - 1 tiles, ranks units or units - 1 units of each
+    for (int64_t n = std::max<int64_t>(1, per - 1); n <= per; ++n)
+      for (int64_t u = nu / C; u <= units; ++u) n_cells = std::max(n_cells, w4_cells(n, u, WARPS));
+    const int64_t sums = C > 1 ? per * out : 0;
+    p.chunk = (int)units;
+    p.pass = (int)per;
+    p.cell_at = (int)(x_fixed + units * x_unit);
+    p.ring_at = p.out_at = (int)(p.cell_at + n_cells * cell);
+    used = p.ring_at + std::max(ring, sums);
+    *fits = used <= kSmemBudget;
+    if (more && (!*fits || tiles * C * 2 <= sms)) continue;
+    if (*fits) break;
+    if (!chunks) return cudaSuccess;
+    // x in chunks, tiles in passes: a pass of t tiles has at most t + WARPS - 1 cells
+    const int64_t room = kSmemBudget - ring - x_fixed - (WARPS - 1) * cell;
+    p.pass = (int)std::max<int64_t>(1, std::min(per, (room / 2) / (out + cell)));
+    p.chunk = (int)std::min<int64_t>(units, (room - p.pass * (out + cell)) / x_unit);
+    if (p.chunk < 1) return cudaErrorInvalidConfiguration;
+    p.out_at = (int)(x_fixed + p.chunk * x_unit);
+    p.cell_at = (int)(p.out_at + p.pass * out);
+    p.ring_at = (int)(p.cell_at + (p.pass + WARPS - 1) * cell);
+    used = p.ring_at + ring;
+    *fits = true;
+    break;
+  }
+  p.tile_q = (int)(tiles / p.clusters);
+  p.tile_r = (int)(tiles % p.clusters);
+  p.unit_q = nu / p.C;
+  p.unit_r = nu % p.C;
+  p.units = nu;
+  p.odd = sqk::w4_blocks(p.K) % 2 != 0;
+  cfg.dynamicSmemBytes = (size_t)used;
+  cfg.gridDim = dim3((unsigned)(p.clusters * p.C), (unsigned)mt);
+  cfg.attrs = p.C > 1 ? attr : attr + 1;
+  cfg.numAttrs = p.C > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <int NT, int S, int WR>
-cudaError_t launch_w4_gemm_g(const sqk::W4GemmParams& p, int group, cudaStream_t st) {
-  if (p.zp) {
-    if (group == 32) return launch_w4_gemm_t<NT, S, 1, true, WR>(p, st);
-    if (group == 64) return launch_w4_gemm_t<NT, S, 2, true, WR>(p, st);
-    return launch_w4_gemm_t<NT, S, 4, true, WR>(p, st);
-  }
-  if (group == 32) return launch_w4_gemm_t<NT, S, 1, false, WR>(p, st);
-  if (group == 64) return launch_w4_gemm_t<NT, S, 2, false, WR>(p, st);
-  return launch_w4_gemm_t<NT, S, 4, false, WR>(p, st);
+template <int NT, int S, int GW, bool ASYM>
+cudaError_t launch_w4_gemm_a(const sqk::W4GemmParams& p, bool chunks, bool* fits, cudaStream_t st) {
+  const bool aligned = p.N % 8 == 0 && (uintptr_t)p.w.scales % 16 == 0 && (uintptr_t)p.w.zeros % 8 == 0;
+  return aligned ? launch_w4_gemm_t<NT, S, GW, ASYM, true>(p, chunks, fits, st)
+                 : launch_w4_gemm_t<NT, S, GW, ASYM, false>(p, chunks, fits, st);
 }
 
-template <int S>
-cudaError_t launch_w4_gemm_m(const sqk::W4GemmParams& p, int group, cudaStream_t st) {
-  if (p.M <= 8) return launch_w4_gemm_g<1, S, 1>(p, group, st);
-  if (p.M <= 16) return launch_w4_gemm_g<2, S, 2>(p, group, st);
-  return launch_w4_gemm_g<4, S, 4>(p, group, st);
+template <int NT, int S>
+cudaError_t launch_w4_gemm_g(const sqk::W4GemmParams& p, int group, bool chunks, bool* fits, cudaStream_t st) {
+  if (p.w.zeros) {
+    if (group == 32) return launch_w4_gemm_a<NT, S, 1, true>(p, chunks, fits, st);
+    if (group == 64) return launch_w4_gemm_a<NT, S, 2, true>(p, chunks, fits, st);
+    return launch_w4_gemm_a<NT, S, 4, true>(p, chunks, fits, st);
+  }
+  if (group == 32) return launch_w4_gemm_a<NT, S, 1, false>(p, chunks, fits, st);
+  if (group == 64) return launch_w4_gemm_a<NT, S, 2, false>(p, chunks, fits, st);
+  return launch_w4_gemm_a<NT, S, 4, false>(p, chunks, fits, st);
 }
 
 }  // namespace
@@ -237,16 +333,27 @@ cudaError_t launch_w4_gemm(const void* x, bool bf16, int64_t M, int64_t K, int64
   p.ldx_bytes = ldx * (bf16 ? 2 : 4);
   p.M = (int)M;
   p.K = (int)K;
-  p.wq = (const char*)wq;
-  p.sg = sg;
-  p.zp = zp;
+  p.w.codes = (const char*)wq;
+  p.w.scales = sg;
+  p.w.zeros = zp;
+  p.w.row_bytes = (uint32_t)(sqk::w4_blocks(K) * sqk::W4_BLOCK_BYTES);
+  p.w.pitch = (uint32_t)N;
+  p.w.groups = (int)((K + group - 1) / group);
   p.N = N;
-  p.row_bytes = sqk::w4_blocks(K) * sqk::W4_BLOCK_BYTES;
-  p.groups = (int)((K + group - 1) / group);
   p.y = y;
   p.ldy = ldy;
   p.y_bf16 = y_bf16;
-  return bf16 ? launch_w4_gemm_m<1>(p, group, st) : launch_w4_gemm_m<3>(p, group, st);
+  bool fits = false;
+  if (bf16) {
+    if (M <= 8) return launch_w4_gemm_g<1, 1>(p, group, true, &fits, st);
+    if (M > 16) {
+      const cudaError_t e = launch_w4_gemm_g<4, 1>(p, group, false, &fits, st);
+      if (e != cudaSuccess || fits) return e;
+    }
+    return launch_w4_gemm_g<2, 1>(p, group, true, &fits, st);
+  }
+  if (M <= 8) return launch_w4_gemm_g<1, 3>(p, group, true, &fits, st);
+  return launch_w4_gemm_g<2, 3>(p, group, true, &fits, st);
 }
 
 }  // namespace sqh
