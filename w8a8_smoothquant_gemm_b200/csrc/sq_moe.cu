@@ -427,10 +427,12 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_up_kernel(const Moe
       if (m >= p.start[a + 1] - s0) continue;
       const float* q = cells + m * RP + f;
       float gate = 0.0f, up = 0.0f;
-      w4_cells_of<MOE_WARPS>(runs, ti, line, inv_line, nb, [&](int c) {
+      const int from = w4_first_cell<MOE_WARPS>(runs, ti, n_tiles, line, inv_line, nb);
+      const int to = w4_first_cell<MOE_WARPS>(runs, ti + 1, n_tiles, line, inv_line, nb);
+      for (int c = from; c < to; ++c) {
         gate = __fadd_rn(gate, q[c * cell_floats]);
         up = __fadd_rn(up, q[c * cell_floats + 8]);
-      });
+      }
       // silu(v) = v / (1 + exp(-v)); exp overflows to inf for very negative v, and v / inf is -0
       const float h = __fmul_rn(__fdiv_rn(gate, __fadd_rn(1.0f, expf(-gate))), up);
       uint32_t part[SH];
@@ -575,8 +577,11 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_down_kernel(const M
     for (int o = tid; o < outs; o += MOE_EXPERT_THREADS) {
       const int row = o % 16, mt = o / 16, ti = mt / p.T, m = mt - ti * p.T;
       float v = 0.0f;
-      if (line > 0)
-        w4_cells_of<MOE_WARPS>(runs, ti, line, inv_line, per_tile, [&](int c) { v = __fadd_rn(v, cells[c * cell_floats + m * RP + row]); });
+      if (line > 0) {
+        const int from = w4_first_cell<MOE_WARPS>(runs, ti, n_tiles, line, inv_line, per_tile);
+        const int to = w4_first_cell<MOE_WARPS>(runs, ti + 1, n_tiles, line, inv_line, per_tile);
+        for (int c = from; c < to; ++c) v = __fadd_rn(v, cells[c * cell_floats + m * RP + row]);
+      }
       const int d = (t0 + p0 + ti) * 16 + row;
       if (p.C > 1) out[o] = v;
       else if (d < p.D) store_out(p.y, m * p.ldy + d, v, p.y_bf16);

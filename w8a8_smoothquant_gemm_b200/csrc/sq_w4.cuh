@@ -274,7 +274,7 @@ constexpr int W4_RP = 20;  // floats between a cell's tokens: 16 rows, padded to
 
 template <int WARPS>
 struct W4Runs {  // in shared memory
-  int first_cell[WARPS], first_tile[WARPS];
+  int first_cell[WARPS], first_tile[WARPS], cells;
 };
 
 // n / d for n < 2^27 with inv = 1 / d: the quotient in binary32 is off by less than one.
@@ -311,6 +311,7 @@ __device__ __forceinline__ W4Run w4_runs(W4Runs<WARPS>& runs, int line, int per_
   if (warp == 0 && lane < WARPS) {
     runs.first_cell[lane] = sum - n;
     runs.first_tile[lane] = at;
+    if (lane == WARPS - 1) runs.cells = sum;
   }
   W4Run r;
   r.units = __shfl_sync(0xffffffffu, a1 - a0, warp);
@@ -320,16 +321,14 @@ __device__ __forceinline__ W4Run w4_runs(W4Runs<WARPS>& runs, int line, int per_
   return r;
 }
 
-// Calls add(cell) for the cells of tile `ti`, in order; inv = 1 / line.
-template <int WARPS, typename Add>
-__device__ __forceinline__ void w4_cells_of(const W4Runs<WARPS>& runs, int ti, int line, float inv, int per_tile,
-                                            Add add) {
-  const int w0 = w4_div(WARPS * (ti * per_tile + 1) - 1, line, inv);
-  const int w1 = w4_div(WARPS * (ti + 1) * per_tile - 1, line, inv);
-#pragma unroll 1
-  for (int w = w0; w <= w1; ++w)
-    if (w4_cut<WARPS>(line, w) != w4_cut<WARPS>(line, w + 1))  // else an empty run
-      add(runs.first_cell[w] + ti - runs.first_tile[w]);
+// The first cell of tile `ti` (of n_tiles; n_tiles itself: the number of cells); inv = 1 / line.
+template <int WARPS>
+__device__ __forceinline__ int w4_first_cell(const W4Runs<WARPS>& runs, int ti, int n_tiles, int line, float inv,
+                                             int per_tile) {
+  if (ti >= n_tiles) return runs.cells;
+  // the run that holds the tile's first unit: w4_cut(w) <= l < w4_cut(w + 1)
+  const int w = w4_div(WARPS * (ti * per_tile + 1) - 1, line, inv);
+  return runs.first_cell[w] + ti - runs.first_tile[w];
 }
 
 // part i of n equal parts of a count whose quotient and remainder by n are q and r: where it begins

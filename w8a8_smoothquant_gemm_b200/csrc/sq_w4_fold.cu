@@ -12,18 +12,19 @@
 // are taken, so the rounding costs no accuracy beyond the grid's own: codes are nearest on the grid
 // that is stored.
 //
-// Bound: one read of W and one write of the codes.  A block takes 128 input channels (one block of
+// Bound: one read of W and one write of the codes.  A block takes 256 input channels (two blocks of
 // the format) of 64 output channels; each thread two output channels and one 32-code word column,
-// so a group's extremes are in registers (group 32) or meet through shared memory once.
+// so a group's extremes are in registers (group 32) or meet through shared memory once, and the two
+// channels' quotients run on packed binary32 pairs (one reciprocal a group, Markstein's correction).
 #include <algorithm>
 
 #include "sq_w4.cuh"
 
 namespace sqk {
 
-constexpr int W4F_COLS = 64;       // output channels per block
-constexpr int W4F_THREADS = 128;   // 32 column pairs x 4 word columns
-constexpr int W4F_PITCH = 64 + 16; // bytes per staged code row (16-byte aligned, spreads the banks)
+constexpr int W4F_COLS = 64;        // output channels per block
+constexpr int W4F_THREADS = 256;    // 32 column pairs x 2 format blocks x 4 word columns
+constexpr int W4F_PITCH = 128 + 16; // bytes per staged code row (16-byte aligned, spreads the banks)
 
 template <bool BF16, bool ASYM>
 __global__ void __launch_bounds__(W4F_THREADS)
@@ -31,114 +32,175 @@ w4_fold_kernel(const char* __restrict__ W, int64_t K, int64_t N, int64_t ld_byte
                const float* __restrict__ gamma, const float* __restrict__ beta, int gw, int groups, int64_t row_bytes,
                char* __restrict__ wq, uint16_t* __restrict__ sg, uint8_t* __restrict__ zp, float* __restrict__ gamma_f,
                float* __restrict__ beta_f) {
-  __shared__ float ext[2][4][W4F_COLS];  // extremes of each 32-code column
+  __shared__ float2 ext[2][8][W4F_COLS / 2];  // extremes of each 32-code column, by column pair
+  __shared__ __align__(16) float factor[W4_UNIT];
   __shared__ __align__(16) char codes[W4F_COLS * W4F_PITCH];
-  const int tid = threadIdx.x, pair = tid % 32, w = tid / 32;
-  const int64_t b = blockIdx.y, n0 = (int64_t)blockIdx.x * W4F_COLS, n = n0 + 2 * pair;
-  const int64_t k0 = b * W4_BLOCK + 32 * w;
-  if (blockIdx.x == 0) {  // LayerNorm folding, one channel per thread
-    const int64_t k = b * W4_BLOCK + tid;
-    if (k < K) {
-      const float sj = s ? s[k] : 1.0f;
+  const int tid = threadIdx.x, pair = tid % 32, col = tid / 32, w = col % 4;
+  const int64_t u0 = (int64_t)blockIdx.y * W4_UNIT, n0 = (int64_t)blockIdx.x * W4F_COLS, n = n0 + 2 * pair;
+  const int64_t k0 = u0 + 32 * col;
+  const int rows = n < N ? (int)max((int64_t)0, min((int64_t)32, K - k0)) : 0;  // rows are whole 16-byte
+  const char* src = W + k0 * ld_bytes + n * (BF16 ? 2 : 4);                     // vectors: N is even
+  uint32_t raw[BF16 ? 32 : 64];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    if (BF16) {
+      raw[i] = i < rows ? __ldg(reinterpret_cast<const uint32_t*>(src + i * ld_bytes)) : 0u;
+    } else {
+      const uint2 v = i < rows ? __ldg(reinterpret_cast<const uint2*>(src + i * ld_bytes)) : make_uint2(0u, 0u);
+      raw[2 * i] = v.x;
+      raw[2 * i + 1] = v.y;
+    }
+  }
+  {
+    const int64_t k = u0 + tid;
+    const float sj = s && k < K ? s[k] : 1.0f;
+    factor[tid] = sj;
+    if (blockIdx.x == 0 && k < K) {  // LayerNorm folding, one channel per thread
       if (gamma && gamma_f) gamma_f[k] = __fdiv_rn(gamma[k], sj);
       if (beta && beta_f) beta_f[k] = __fdiv_rn(beta[k], sj);
     }
   }
-  float v[2][32];
-  float top[2] = {0.0f, 0.0f}, bot[2] = {0.0f, 0.0f};
+  __syncthreads();
+  float2 v[32];
+  float2 top = make_float2(0.0f, 0.0f), bot = top;  // for symmetric scales, top is the largest magnitude
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    v[0][i] = v[1][i] = 0.0f;
-    if (k0 + i < K && n < N) {  // rows are whole 16-byte vectors, so a pair never straddles the end
-      const float sj = s ? __ldg(s + k0 + i) : 1.0f;
-      if (BF16) {
-        const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(W + (k0 + i) * ld_bytes + n * 2));
-        v[0][i] = __fmul_rn(sj, bf16lo(u));
-        v[1][i] = __fmul_rn(sj, bf16hi(u));
+  for (int i = 0; i < 32; i += 4) {
+    const float4 f = *reinterpret_cast<const float4*>(factor + 32 * col + i);
+    const float fi[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 a = BF16 ? make_float2(bf16lo(raw[i + j]), bf16hi(raw[i + j]))
+                            : make_float2(__uint_as_float(raw[BF16 ? 0 : 2 * (i + j)]), __uint_as_float(raw[BF16 ? 0 : 2 * (i + j) + 1]));
+      v[i + j] = __fmul2_rn(make_float2(fi[j], fi[j]), a);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      const float2 p = v[i + j], q = v[i + j + 1];
+      if (ASYM) {
+        top = make_float2(fmax3(top.x, p.x, q.x), fmax3(top.y, p.y, q.y));
+        bot = make_float2(-fmax3(-bot.x, -p.x, -q.x), -fmax3(-bot.y, -p.y, -q.y));
       } else {
-        const float2 u = __ldg(reinterpret_cast<const float2*>(W + (k0 + i) * ld_bytes + n * 4));
-        v[0][i] = __fmul_rn(sj, u.x);
-        v[1][i] = __fmul_rn(sj, u.y);
+        top = make_float2(fmax3(top.x, fabsf(p.x), fabsf(q.x)), fmax3(top.y, fabsf(p.y), fabsf(q.y)));
       }
     }
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      top[c] = fmaxf(top[c], v[c][i]);
-      bot[c] = fminf(bot[c], v[c][i]);
-    }
   }
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    ext[0][w][2 * pair + c] = top[c];
-    ext[1][w][2 * pair + c] = bot[c];
-  }
-  __syncthreads();
-  const int g0 = w / gw * gw;  // first word column of this thread's group
-  const int64_t gidx = b * (4 / gw) + w / gw;
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
+  if (gw > 1) {
+    ext[0][col][pair] = top;
+    if (ASYM) ext[1][col][pair] = bot;
+    __syncthreads();
+    const int g0 = col / gw * gw;  // first word column of this thread's group
     for (int q = g0; q < g0 + gw; ++q) {
-      top[c] = fmaxf(top[c], ext[0][q][2 * pair + c]);
-      bot[c] = fminf(bot[c], ext[1][q][2 * pair + c]);
-    }
-    float scale = ASYM ? __fdiv_rn(__fsub_rn(top[c], bot[c]), 15.0f) : __fdiv_rn(fmaxf(top[c], -bot[c]), 7.0f);
-    const __nv_bfloat16 sb = __float2bfloat16_rn(scale);
-    scale = __bfloat162float(sb);
-    float zero = 8.0f;
-    if (ASYM) zero = scale == 0.0f ? 0.0f : fminf(fmaxf(rintf(__fdiv_rn(-bot[c], scale)), 0.0f), 15.0f);
-    const SharedDivisor d(scale);
-    uint32_t word[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float q = rintf(d.div(v[c][i]));
-      const float code = ASYM ? fminf(fmaxf(__fadd_rn(q, zero), 0.0f), 15.0f) : __fadd_rn(fminf(fmaxf(q, -7.0f), 7.0f), 8.0f);
-      const uint32_t u = k0 + i < K ? (uint32_t)(int)code : 0u;  // padding of the last block
-      word[i / 8] |= u << (4 * ((i % 8) / 2) + 16 * (i % 2));
-    }
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      *reinterpret_cast<uint32_t*>(codes + (2 * pair + c) * W4F_PITCH + 16 * t + 4 * w) = word[t];
-    if (w == g0 && gidx < groups && n + c < N) {
-      sg[gidx * N + n + c] = __bfloat16_as_ushort(sb);
-      if (ASYM) zp[gidx * N + n + c] = (uint8_t)(int)zero;
+      const float2 e = ext[0][q][pair];
+      top = make_float2(fmaxf(top.x, e.x), fmaxf(top.y, e.y));
+      if (ASYM) {
+        const float2 d = ext[1][q][pair];
+        bot = make_float2(fminf(bot.x, d.x), fminf(bot.y, d.y));
+      }
     }
   }
+  const float2 range = ASYM ? make_float2(__fdiv_rn(__fsub_rn(top.x, bot.x), 15.0f), __fdiv_rn(__fsub_rn(top.y, bot.y), 15.0f))
+                            : make_float2(__fdiv_rn(top.x, 7.0f), __fdiv_rn(top.y, 7.0f));
+  const __nv_bfloat16 sb[2] = {__float2bfloat16_rn(range.x), __float2bfloat16_rn(range.y)};
+  const float2 scale = make_float2(__bfloat162float(sb[0]), __bfloat162float(sb[1]));
+  float2 zero = make_float2(8.0f, 8.0f);
+  if (ASYM) {
+    zero.x = scale.x == 0.0f ? 0.0f : fminf(rintf(__fdiv_rn(-bot.x, scale.x)), 15.0f);
+    zero.y = scale.y == 0.0f ? 0.0f : fminf(rintf(__fdiv_rn(-bot.y, scale.y)), 15.0f);
+  }
+  const SharedDivisor dx(scale.x), dy(scale.y);
+  uint32_t wx[4], wy[4];
+  if (dx.fast && dy.fast) {
+    // Adding 1.5 * 2^23 + zero rounds the quotient to an integer, ties to even, and leaves the code
+    // in the low bits of the sum (0x4b400000 + code).  The quotient lies within 1 + 2^-8 (the scale's
+    // rounding to bf16) of the codes' range: below 7.03 of a symmetric grid's 7.5, and never below
+    // rne(lo / scale) = -zero; only the upper end of a grid with a zero point can need the clip.
+    const float2 rc = make_float2(dx.y, dy.y), nb = make_float2(-dx.b, -dy.b);
+    const float2 magic = make_float2(12582912.0f + zero.x, 12582912.0f + zero.y);
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+      uint32_t ax = 0u, ay = 0u;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float2 t = __fadd2_rn(markstein2(v[i + j], rc, nb), magic);
+        if (ASYM) t = make_float2(fminf(t.x, 12582927.0f), fminf(t.y, 12582927.0f));
+        const int sh = 4 * (j / 2) + 16 * (j % 2);
+        ax += (__float_as_uint(t.x) - 0x4b400000u) << sh;
+        ay += (__float_as_uint(t.y) - 0x4b400000u) << sh;
+      }
+      wx[i / 8] = ax;
+      wy[i / 8] = ay;
+    }
+  } else {  // rare: a scale outside the fast range (its rounding to bf16 may then be coarse)
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+      uint32_t ax = 0u, ay = 0u;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int sh = 4 * (j / 2) + 16 * (j % 2);
+        const float qx = rintf(dx.div(v[i + j].x)), qy = rintf(dy.div(v[i + j].y));
+        const float cx = ASYM ? fminf(fmaxf(__fadd_rn(qx, zero.x), 0.0f), 15.0f) : fminf(fmaxf(qx, -7.0f), 7.0f) + 8.0f;
+        const float cy = ASYM ? fminf(fmaxf(__fadd_rn(qy, zero.y), 0.0f), 15.0f) : fminf(fmaxf(qy, -7.0f), 7.0f) + 8.0f;
+        ax |= (uint32_t)(int)cx << sh;
+        ay |= (uint32_t)(int)cy << sh;
+      }
+      wx[i / 8] = ax;
+      wy[i / 8] = ay;
+    }
+  }
+  const int64_t gidx = (blockIdx.y * 8 + col) / gw;
+  if (col % gw == 0 && gidx < groups && rows > 0) {
+    reinterpret_cast<uint16_t*>(sg)[gidx * N + n] = __bfloat16_as_ushort(sb[0]);
+    reinterpret_cast<uint16_t*>(sg)[gidx * N + n + 1] = __bfloat16_as_ushort(sb[1]);
+    if (ASYM) {
+      zp[gidx * N + n] = (uint8_t)(int)zero.x;
+      zp[gidx * N + n + 1] = (uint8_t)(int)zero.y;
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const bool there = 8 * t < rows;  // channels come in sixteens; the padding of the last block is 0
+    char* at = codes + 2 * pair * W4F_PITCH + (col / 4) * W4_BLOCK_BYTES + 16 * t + 4 * w;
+    *reinterpret_cast<uint32_t*>(at) = there ? wx[t] : 0u;
+    *reinterpret_cast<uint32_t*>(at + W4F_PITCH) = there ? wy[t] : 0u;
+  }
   __syncthreads();
-  for (int i = tid; i < W4F_COLS * 4; i += W4F_THREADS) {
-    const int row = i / 4, t = i % 4;
-    if (n0 + row < N)
-      *reinterpret_cast<uint4*>(wq + (n0 + row) * row_bytes + b * W4_BLOCK_BYTES + 16 * t) =
+  const int64_t b0 = (int64_t)blockIdx.y * (2 * W4_BLOCK_BYTES);
+#pragma unroll
+  for (int i = tid; i < W4F_COLS * 8; i += W4F_THREADS) {
+    const int row = i / 8, t = i % 8;
+    if (n0 + row < N && b0 + 16 * t < row_bytes)
+      *reinterpret_cast<uint4*>(wq + (n0 + row) * row_bytes + b0 + 16 * t) =
           *reinterpret_cast<const uint4*>(codes + row * W4F_PITCH + 16 * t);
   }
 }
 
 // Values: (code - zero) * scale, at most 12 significant bits (exact in binary32), rounded once for
-// bf16.  One thread per 16 bytes of codes: four runs of 8 consecutive k.
+// bf16.  One thread per 16 bytes of codes: four runs of 8 consecutive k.  A warp takes 32 pieces of
+// one row, so both sides are whole lines.
 template <bool BF16>
 __global__ void __launch_bounds__(256)
-w4_dequant_kernel(const char* __restrict__ wq, const uint16_t* __restrict__ sg, const uint8_t* __restrict__ zp,
-                  int64_t K, int64_t N, int gw, int groups, int64_t row_bytes, char* __restrict__ y, int64_t ld_bytes) {
-  const int64_t pieces = row_bytes / 16;
-  const int64_t total = pieces * N;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t n = i / pieces, piece = i % pieces, b = piece / 4;
-    const int t = (int)(piece % 4);
+w4_dequant_kernel(const char* __restrict__ wq, const uint16_t* __restrict__ sg, const uint8_t* __restrict__ zp, int K,
+                  int64_t N, int gw, int row_bytes, char* __restrict__ y, int64_t ld_bytes) {
+  const int piece = blockIdx.x * 32 + threadIdx.x % 32, b = piece / 4, t = piece % 4;
+  if (piece * 16 >= row_bytes) return;
+  for (int64_t n = (int64_t)blockIdx.y * 8 + threadIdx.x / 32; n < N; n += (int64_t)gridDim.y * 8) {
     const uint4 c = ldg_stream16(wq + n * row_bytes + piece * 16);
     const uint32_t word[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const int64_t k = b * W4_BLOCK + 32 * w + 8 * t;
+      const int k = b * W4_BLOCK + 32 * w + 8 * t;
       if (k >= K) continue;
-      const int64_t g = (b * (4 / gw) + w / gw) * N + n;
+      const int64_t g = (int64_t)(b * (4 / gw) + w / gw) * N + n;
       const float scale = __uint_as_float((uint32_t)__ldg(sg + g) << 16);
-      const int zero = zp ? (int)__ldg(zp + g) : 8;
+      // 2^23 + code, minus 2^23 + zero: exact
+      const float zero = 8388608.0f + (zp ? (float)__ldg(zp + g) : 8.0f);
       float f[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int code = (int)((word[w] >> (4 * (e / 2) + 16 * (e % 2))) & 15u);
-        f[e] = __fmul_rn((float)(code - zero), scale);
+        const uint32_t code = (word[w] >> (4 * (e / 2) + 16 * (e % 2))) & 15u;
+        f[e] = __fmul_rn(__fsub_rn(__uint_as_float(0x4b000000u | code), zero), scale);
       }
-      char* out = y + n * ld_bytes + k * (BF16 ? 2 : 4);
+      char* out = y + n * ld_bytes + (int64_t)k * (BF16 ? 2 : 4);
       if (BF16) {
         uint32_t o[4];
 #pragma unroll
@@ -146,10 +208,10 @@ w4_dequant_kernel(const char* __restrict__ wq, const uint16_t* __restrict__ sg, 
           const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
           o[e] = *reinterpret_cast<const uint32_t*>(&h);
         }
-        *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
+        __stcs(reinterpret_cast<uint4*>(out), make_uint4(o[0], o[1], o[2], o[3]));
       } else {
-        *reinterpret_cast<float4*>(out) = make_float4(f[0], f[1], f[2], f[3]);
-        *reinterpret_cast<float4*>(out + 16) = make_float4(f[4], f[5], f[6], f[7]);
+        __stcs(reinterpret_cast<float4*>(out), make_float4(f[0], f[1], f[2], f[3]));
+        __stcs(reinterpret_cast<float4*>(out + 16), make_float4(f[4], f[5], f[6], f[7]));
       }
     }
   }
@@ -162,9 +224,9 @@ namespace sqh {
 cudaError_t launch_w4_fold(const void* W, bool bf16, int64_t K, int64_t N, int64_t ldw, const float* s,
                            const float* gamma, const float* beta, int group, uint8_t* wq, uint16_t* sg, uint8_t* zp,
                            float* gamma_f, float* beta_f, cudaStream_t st) {
-  const int64_t nb = sqk::w4_blocks(K), row_bytes = nb * sqk::W4_BLOCK_BYTES, ldb = ldw * (bf16 ? 2 : 4);
+  const int64_t row_bytes = sqk::w4_blocks(K) * sqk::W4_BLOCK_BYTES, ldb = ldw * (bf16 ? 2 : 4);
   const int gw = group / 32, groups = (int)((K + group - 1) / group);
-  const dim3 grid((unsigned)((N + sqk::W4F_COLS - 1) / sqk::W4F_COLS), (unsigned)nb);
+  const dim3 grid((unsigned)((N + sqk::W4F_COLS - 1) / sqk::W4F_COLS), (unsigned)sqk::w4_units(K));
   auto go = [&](auto kern) {
     kern<<<grid, sqk::W4F_THREADS, 0, st>>>((const char*)W, K, N, ldb, s, gamma, beta, gw, groups, row_bytes,
                                             (char*)wq, sg, zp, gamma_f, beta_f);
@@ -176,15 +238,12 @@ cudaError_t launch_w4_fold(const void* W, bool bf16, int64_t K, int64_t N, int64
 
 cudaError_t launch_w4_dequant(const uint8_t* wq, const uint16_t* sg, const uint8_t* zp, int64_t K, int64_t N, int group,
                               void* y, bool y_bf16, int64_t ldy, cudaStream_t st) {
-  const int64_t row_bytes = sqk::w4_blocks(K) * sqk::W4_BLOCK_BYTES, total = row_bytes / 16 * N;
-  const int groups = (int)((K + group - 1) / group);
-  const unsigned grid = (unsigned)std::min<int64_t>((total + 255) / 256, (int64_t)num_sms() * 64);
-  if (y_bf16)
-    sqk::w4_dequant_kernel<true><<<grid, 256, 0, st>>>((const char*)wq, sg, zp, K, N, group / 32, groups, row_bytes,
-                                                       (char*)y, ldy * 2);
-  else
-    sqk::w4_dequant_kernel<false><<<grid, 256, 0, st>>>((const char*)wq, sg, zp, K, N, group / 32, groups, row_bytes,
-                                                        (char*)y, ldy * 4);
+  const int row_bytes = (int)(sqk::w4_blocks(K) * sqk::W4_BLOCK_BYTES);
+  const dim3 grid((unsigned)((row_bytes / 16 + 31) / 32), (unsigned)std::min<int64_t>((N + 7) / 8, 65535));
+  auto go = [&](auto kern) {
+    kern<<<grid, 256, 0, st>>>((const char*)wq, sg, zp, (int)K, N, group / 32, row_bytes, (char*)y, ldy * (y_bf16 ? 2 : 4));
+  };
+  y_bf16 ? go(sqk::w4_dequant_kernel<true>) : go(sqk::w4_dequant_kernel<false>);
   return cudaGetLastError();
 }
 

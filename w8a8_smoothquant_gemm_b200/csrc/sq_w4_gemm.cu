@@ -179,14 +179,18 @@ __global__ void __launch_bounds__(32 * W4G_WARPS, 1) w4_gemm_kernel(const W4Gemm
         }
       }
       __syncthreads();
-      const int outs = n_tiles * Mr * 16;
+      // 16 rows x 8 NT tokens a tile
       const float inv_line = __frcp_rn((float)line);
       const bool last = c0 + p.chunk >= b1;
-      for (int o = tid; o < outs; o += THREADS) {
-        const int row = o % 16, mt = o / 16, ti = mt / Mr, m = mt - ti * Mr;
-        const float* q = cells + m * RP + row;
+      const int row = tid % 16, m = tid / 16 % (8 * NT);
+      for (int ti = tid / (128 * NT); ti < n_tiles; ti += THREADS / (128 * NT)) {
+        const int from = w4_first_cell<WARPS>(runs, ti, n_tiles, line, inv_line, units);
+        const int to = w4_first_cell<WARPS>(runs, ti + 1, n_tiles, line, inv_line, units);
+        if (m >= Mr) continue;
+        const float* q = cells + (from * Mr + m) * RP + row;
+        const int o = (ti * Mr + m) * 16 + row;
         float v = c0 == b0 ? 0.0f : out[o];
-        w4_cells_of<WARPS>(runs, ti, line, inv_line, units, [&](int c) { v = __fadd_rn(v, q[c * Mr * RP]); });
+        for (int c = from; c < to; ++c, q += Mr * RP) v = __fadd_rn(v, *q);
         const int64_t n = (t0 + p0 + ti) * 16 + row;
         if (p.C > 1 || !last) out[o] = v;
         else if (n < p.N) store_out(p.y, (m0 + m) * p.ldy + n, v, p.y_bf16);
@@ -195,8 +199,9 @@ __global__ void __launch_bounds__(32 * W4G_WARPS, 1) w4_gemm_kernel(const W4Gemm
     if (p.C > 1) {
       cluster_sync();
       const int outs = n_tiles * Mr * 16;
+      const float inv_Mr = __frcp_rn((float)Mr);
       for (int o = rank * THREADS + tid; o < outs; o += p.C * THREADS) {
-        const int row = o % 16, mt = o / 16, ti = mt / Mr, m = mt - ti * Mr;
+        const int row = o % 16, mt = o / 16, ti = w4_div(mt, Mr, inv_Mr), m = mt - ti * Mr;
         float v = ld_dsmem_f32(out + o, 0);
         for (int c = 1; c < p.C; ++c) v = __fadd_rn(v, ld_dsmem_f32(out + o, c));
         const int64_t n = (t0 + p0 + ti) * 16 + row;
