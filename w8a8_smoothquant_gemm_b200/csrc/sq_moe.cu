@@ -5,14 +5,16 @@
 //   y[t]         = sum over the chosen e of weight[t, e] * (W2_e h[t, e])
 //
 // Bound: the chosen experts' codes, each read once from HBM.  Three kernels, chained as
-// programmatic dependents: the router (its last block builds the lists), gate/up, down.  The work
-// is cut by (expert, rows), never by token: an expert's weights are read once for all of its
-// tokens, which are the columns of the mma (sq_w4.cuh).
-//   Router sums are binary64, so that which experts are chosen does not hang on rounding.  h is
+// programmatic dependents: router logits; choice, gate and up; down.  The work is cut by (expert,
+// rows), never by token: an expert's weights are read once for all of its tokens, which are the
+// columns of the mma (sq_w4.cuh).
+//   Router sums are binary64, so that which experts are chosen does not hang on rounding.  Every CTA
+// of the gate/up kernel makes the choice for itself from the logits (a warp per token, a few hundred
+// cycles), which is shorter than one block doing it for all behind another pair of fences.  h is
 // kept as two bf16 parts (16 significant bits; three for a binary32 layer), so the only bf16
 // rounding of the layer is the final store.  Every sum has a fixed order; the only atomics are the
-// lists' bit masks (order-free) and the router's arrival count.  The expert kernels are one CTA per
-// SM with the weight stream of sq_w4.cuh.
+// lists' bit masks (order-free).  The expert kernels are one CTA per SM with the weight stream of
+// sq_w4.cuh.
 #include <algorithm>
 
 #include "sq_w4.cuh"
@@ -22,13 +24,7 @@ namespace sqk {
 constexpr int MOE_MAX_T = 64;    // tokens: one bit each of an expert's token mask
 constexpr int MOE_MAX_E = 1024;  // experts
 constexpr int MOE_MAX_K = 32;    // choices per token
-constexpr int MOE_THREADS = 256;
-constexpr int MOE_ENTRY = 32;    // tokens of an entry: four column tiles of the mma
-
-struct MoeLists {  // in the workspace, written by the router (or from given choices)
-  unsigned int arrived;  // router blocks that are done; wraps to 0 by itself
-  int active;            // entries: experts with tokens, MOE_ENTRY of them at a time
-};
+constexpr int MOE_ENTRY = 32;    // most tokens of an entry: four column tiles of the mma
 
 struct MoeParams {
   const char* x;
@@ -49,91 +45,117 @@ struct MoeParams {
   int64_t ldy;
   int y_bf16;
   // workspace
-  MoeLists* lists;
   double* logits;       // [T, E]
-  int* expert;          // [active] expert of an entry
-  int* start;           // [active + 1] its first slot; the slots of an expert's entries follow one another
-  int* slot_token;      // [T k]
-  float* slot_weight;   // [T k]
+  int* lists;           // see MoeLists
   uint16_t* xparts;     // [3, T, D] (binary32 x)
   uint16_t* h;          // [parts, T k, F]
   // the expert kernels' shared memory
+  int entries;          // most entries of the lists
   bool x_staged;        // x in shared memory
-  int up_cells_at, up_ring_at, up_pass;  // tiles whose cells fit
-  int down_ring_at, down_pass;
+  int up_x_at, up_cells_at, up_ring_at, up_pass;  // the lists come first; pass: tiles whose cells fit
+  int down_cells_at, down_ring_at, down_pass;
   int C;                // CTAs of the down kernel's cluster
 };
 
+constexpr int MOE_DEPTH = 3;   // slots of a warp's ring
+constexpr int MOE_WARPS = 16;  // of an expert kernel's CTA
+constexpr int MOE_EXPERT_THREADS = 32 * MOE_WARPS;
+constexpr int MOE_LOGIT_WARPS = 8;
+
 // ---------------------------------------------------------------------------- lists
-struct MoeShared {
-  unsigned long long mask[MOE_MAX_E];
-  int offset[MOE_MAX_E];
-  int scan[MOE_THREADS];
+// Entries (an expert and up to MOE_ENTRY of its tokens), and slots (a token of an expert), which lie
+// in the order of the experts and, for one expert, of the tokens.  All in one array of ints, so that
+// the down kernel can copy it as it is.
+struct MoeLists {
+  int* active;  // number of entries
+  int* expert;  // [entries]
+  int* start;   // [entries + 1] first slot
+  int* token;   // [T k] of a slot
+  float* weight;
+  __host__ __device__ MoeLists(int* at, int entries, int slots)
+      : active(at), expert(at + 1), start(expert + entries), token(start + entries + 1),
+        weight(reinterpret_cast<float*>(token + slots)) {}
+  __host__ __device__ static int64_t ints(int64_t entries, int64_t slots) { return 2 + 2 * entries + 2 * slots; }
 };
 
-// Builds the expert lists from the choices in `ids`, `wts` [T, k] (one block).  A choice outside
+// What building them needs for a while.
+struct MoeScratch {
+  unsigned long long* mask;  // [E] tokens of an expert
+  int* offset;               // [E] its first slot
+  int* ids;                  // [T k]
+  float* wts;                // [T k]
+  __device__ MoeScratch(char* at, int E, int slots)
+      : mask(reinterpret_cast<unsigned long long*>(at)), offset(reinterpret_cast<int*>(mask + E)), ids(offset + E),
+        wts(reinterpret_cast<float*>(ids + slots)) {}
+  __host__ __device__ static int64_t bytes(int64_t E, int64_t slots) { return 12 * E + 8 * slots; }
+};
+
+// Builds the lists from the choices in `sc` (a block of MOE_EXPERT_THREADS).  A choice outside
 // [0, E) is left out; one that a token names twice counts once, with the weights' sum.
-__device__ void moe_build_lists(const MoeParams& p, MoeShared& sh, const int* ids, const float* wts) {
-  const int tid = threadIdx.x;
-  for (int e = tid; e < p.E; e += MOE_THREADS) sh.mask[e] = 0ull;
+__device__ void moe_build_lists(const MoeParams& p, const MoeLists& l, const MoeScratch& sc, int* warp_sums) {
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  for (int e = tid; e < p.E; e += MOE_EXPERT_THREADS) sc.mask[e] = 0ull;
   __syncthreads();
   const int pairs = p.T * p.top_k;
-  for (int i = tid; i < pairs; i += MOE_THREADS) {
-    const int e = ids[i];
-    if (e >= 0 && e < p.E) atomicOr(&sh.mask[e], 1ull << (i / p.top_k));
+  for (int i = tid; i < pairs; i += MOE_EXPERT_THREADS) {
+    const int e = sc.ids[i];
+    if (e >= 0 && e < p.E) atomicOr(&sc.mask[e], 1ull << (i / p.top_k));
   }
   __syncthreads();
-  // exclusive sums of tokens and of entries: a run of experts per thread, then a scan
-  const int per = (p.E + MOE_THREADS - 1) / MOE_THREADS;
-  int tokens = 0, active = 0;
+  // exclusive sums of tokens (low half) and of entries (high half) over the experts, a run of them per
+  // thread: at most 2048 of either
+  const int per = (p.E + MOE_EXPERT_THREADS - 1) / MOE_EXPERT_THREADS;
+  int mine = 0;
   for (int e = tid * per; e < min(p.E, (tid + 1) * per); ++e) {
-    const int c = __popcll(sh.mask[e]);
-    tokens += c;
-    active += (c + MOE_ENTRY - 1) / MOE_ENTRY;
+    const int c = __popcll(sc.mask[e]);
+    mine += c + ((c + MOE_ENTRY - 1) / MOE_ENTRY << 16);
   }
-  int packed = tokens | (active << 16);  // at most 2048 slots and as many entries
-  sh.scan[tid] = packed;
+  int sum = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int v = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += v;
+  }
+  if (lane == 31) warp_sums[warp] = sum;
   __syncthreads();
-  for (int o = 1; o < MOE_THREADS; o *= 2) {
-    const int v = tid >= o ? sh.scan[tid - o] : 0;
-    __syncthreads();
-    sh.scan[tid] += v;
-    __syncthreads();
+  int before = sum - mine, total = 0;
+  for (int w = 0; w < MOE_WARPS; ++w) {
+    const int v = warp_sums[w];
+    before += w < warp ? v : 0;
+    total += v;
   }
-  const int before = sh.scan[tid] - packed;
-  tokens = before & 0xffff;
-  active = before >> 16;
+  int tokens = before & 0xffff, active = before >> 16;
   for (int e = tid * per; e < min(p.E, (tid + 1) * per); ++e) {
-    const int c = __popcll(sh.mask[e]);
-    sh.offset[e] = tokens;
+    const int c = __popcll(sc.mask[e]);
+    sc.offset[e] = tokens;
     for (int first = 0; first < c; first += MOE_ENTRY) {
-      p.expert[active] = e;
-      p.start[active] = tokens + first;
+      l.expert[active] = e;
+      l.start[active] = tokens + first;
       ++active;
     }
     tokens += c;
   }
-  if (tid == MOE_THREADS - 1) {
-    const int total = sh.scan[tid];
-    p.lists->active = total >> 16;
-    p.start[total >> 16] = total & 0xffff;
+  if (tid == 0) {
+    *l.active = total >> 16;
+    l.start[total >> 16] = total & 0xffff;
   }
   __syncthreads();
-  for (int i = tid; i < pairs; i += MOE_THREADS) {
-    const int e = ids[i], t = i / p.top_k, first = t * p.top_k;
+  for (int i = tid; i < pairs; i += MOE_EXPERT_THREADS) {
+    const int e = sc.ids[i], t = i / p.top_k, first = t * p.top_k;
     if (e < 0 || e >= p.E) continue;
     float w = 0.0f;
     bool earlier = false;
     for (int j = first; j < first + p.top_k; ++j) {
-      if (ids[j] != e) continue;
+      if (sc.ids[j] != e) continue;
       earlier |= j < i;
-      w = __fadd_rn(w, wts[j]);
+      w = __fadd_rn(w, sc.wts[j]);
     }
     if (earlier) continue;
-    const int slot = sh.offset[e] + __popcll(sh.mask[e] & ((1ull << t) - 1ull));
-    p.slot_token[slot] = t;
-    p.slot_weight[slot] = w;
+    const int slot = sc.offset[e] + __popcll(sc.mask[e] & ((1ull << t) - 1ull));
+    l.token[slot] = t;
+    l.weight[slot] = w;
   }
+  __syncthreads();
 }
 
 // ---------------------------------------------------------------------------- router
@@ -153,119 +175,127 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
-// The k largest logits of one token, by one warp: ties to the lowest index, NaN counts as -inf.
-__device__ void moe_choose(const MoeParams& p, int t, int lane) {
-  constexpr int PER = MOE_MAX_E / 32;
-  const double* row = p.logits + (int64_t)t * p.E;
-  const double none = -__longlong_as_double(0x7ff0000000000000ll);
-  unsigned int taken = 0u;  // one bit per value of this lane
-  double top = none;
-  bool nan = false;
-  for (int i = 0; i < PER; ++i) {
-    const int e = i * 32 + lane;
-    if (e >= p.E) break;
-    const double v = row[e];
-    nan |= v != v;
-    top = v > top ? v : top;
+// Logits of EB experts and TB tokens by one block, its 8 warps and their lanes along D.  Bound by the
+// conversions to binary64 (EB + TB of them for EB TB multiply-adds).
+template <bool XB, bool RB, int EB, int TB>
+__global__ void __launch_bounds__(32 * MOE_LOGIT_WARPS) moe_logits_kernel(const MoeParams p) {
+  __shared__ double part[MOE_LOGIT_WARPS][EB * TB];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int e0 = blockIdx.x * EB, t0 = blockIdx.y * TB;
+  wait_for_previous_kernel();
+  allow_dependent_launch();
+  double sum[EB][TB] = {};
+  for (int d = tid * 8; d < p.D; d += MOE_LOGIT_WARPS * 256) {
+    float w[EB][8];
+#pragma unroll
+    for (int e = 0; e < EB; ++e)  // experts and tokens past the end repeat the last one, not stored
+      load8<RB>(p.wr + ((int64_t)min(e0 + e, p.E - 1) * p.D + d) * (RB ? 2 : 4), w[e]);
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+      float x[8];
+      load8<XB>(p.x + min(t0 + t, p.T - 1) * p.ldx_bytes + (int64_t)d * (XB ? 2 : 4), x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < EB; ++e) sum[e][t] = fma((double)x[i], (double)w[e][i], sum[e][t]);
+    }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o /= 2) {
-    const double v = __shfl_xor_sync(0xffffffffu, top, o);
-    top = v > top ? v : top;
+  for (int e = 0; e < EB; ++e)
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+      const double v = warp_sum(sum[e][t]);
+      if (lane == 0) part[warp][e * TB + t] = v;
+    }
+  __syncthreads();
+  if (tid < EB * TB) {
+    double v = part[0][tid];
+#pragma unroll
+    for (int i = 1; i < MOE_LOGIT_WARPS; ++i) v += part[i][tid];
+    const int e = e0 + tid / TB, t = t0 + tid % TB;
+    if (e < p.E && t < p.T) p.logits[(int64_t)t * p.E + e] = v;
   }
-  nan = __any_sync(0xffffffffu, nan);
-  double sum = 0.0;
+}
+
+// The k largest logits of one token, by one warp, PER of them a lane: ties to the lowest index, NaN
+// ranks last.  Compared as integers of the same order (0: none, 1: NaN).
+template <int PER>
+__device__ __noinline__ void moe_choose(const MoeParams& p, const MoeScratch& sc, int t, int lane) {
+  const double* row = p.logits + (int64_t)t * p.E;
+  double v[PER];
+  unsigned long long key[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) v[i] = i * 32 + lane < p.E ? row[i * 32 + lane] : 0.0;
+#pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int e = i * 32 + lane;
-    if (e >= p.E) break;
-    sum += (double)expf((float)(row[e] - top));
+    const unsigned long long b = (unsigned long long)__double_as_longlong(v[i]);
+    key[i] = i * 32 + lane >= p.E ? 0ull : v[i] != v[i] ? 1ull : b >> 63 ? ~b : b | 1ull << 63;
   }
-  sum = warp_sum(sum);
-  double chosen_sum = 0.0, mine = 0.0;
+  double top = 0.0, best = 0.0, mine = 0.0;
   int my_id = 0;
   for (int j = 0; j < p.top_k; ++j) {
-    double best = none;
-    int at = INT32_MAX;
-    for (int i = 0; i < PER; ++i) {
-      const int e = i * 32 + lane;
-      if (e >= p.E) break;
-      if (taken >> i & 1u) continue;
-      const double v = row[e];
-      if (at == INT32_MAX || v > best) {
-        best = v == v ? v : none;
-        at = e;
-      }
-    }
+    unsigned long long k = key[0];
+    int at = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2) {
-      const double v = __shfl_xor_sync(0xffffffffu, best, o);
-      const int a = __shfl_xor_sync(0xffffffffu, at, o);
-      if (a != INT32_MAX && (at == INT32_MAX || v > best || (v == best && a < at))) {
-        best = v;
-        at = a;
-      }
+    for (int i = 1; i < PER; ++i) {
+      at = key[i] > k ? i : at;
+      k = key[i] > k ? key[i] : k;
     }
-    if (at % 32 == lane) taken |= 1u << (at / 32);
-    const double w = nan ? __longlong_as_double(0x7ff8000000000000ll) : (double)expf((float)(best - top)) / sum;
-    chosen_sum += w;
+    const uint32_t hi = (uint32_t)(k >> 32), hi_max = __reduce_max_sync(0xffffffffu, hi);
+    const uint32_t lo = hi == hi_max ? (uint32_t)k : 0u, lo_max = __reduce_max_sync(0xffffffffu, lo);
+    const bool tied = hi == hi_max && (uint32_t)k == lo_max;
+    const int id = (int)__reduce_min_sync(0xffffffffu, tied ? (uint32_t)(at * 32 + lane) : 0xffffffffu);
+    const unsigned long long w = (unsigned long long)hi_max << 32 | lo_max;
+    best = w == 1ull ? __longlong_as_double(0x7ff8000000000000ll)
+                     : __longlong_as_double((long long)(w >> 63 ? w & ~(1ull << 63) : ~w));
+    if (j == 0) top = best;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (i * 32 + lane == id) key[i] = 0ull;
     if (j == lane) {
-      mine = w;
-      my_id = at;
+      mine = best;
+      my_id = id;
     }
   }
-  if (lane < p.top_k) {
-    p.ids[t * p.top_k + lane] = my_id;
-    p.wts[t * p.top_k + lane] = (float)(p.renorm ? mine / chosen_sum : mine);
-  }
-}
-
-// Block (e, token block): logits of one expert, tokens in turn; the 8 warps split D.
-template <bool XB, bool RB>
-__global__ void __launch_bounds__(MOE_THREADS) moe_router_kernel(const MoeParams p) {
-  __shared__ MoeShared sh;
-  __shared__ double part[8];
-  __shared__ bool last;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  wait_for_previous_kernel();
-  allow_dependent_launch();
-  const int e = blockIdx.x;
-  const char* wrow = p.wr + (int64_t)e * p.D * (RB ? 2 : 4);
-  for (int t = blockIdx.y; t < p.T; t += gridDim.y) {
-    double sum = 0.0;
-    for (int d = tid * 8; d < p.D; d += MOE_THREADS * 8) {
-      float a[8], w[8];
-      load8<XB>(p.x + t * p.ldx_bytes + (int64_t)d * (XB ? 2 : 4), a);
-      load8<RB>(wrow + (int64_t)d * (RB ? 2 : 4), w);
+  double sum = 0.0;  // a NaN logit makes it, and so every weight, NaN
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fma((double)a[i], (double)w[i], sum);
-    }
-    sum = warp_sum(sum);
-    if (lane == 0) part[warp] = sum;
-    __syncthreads();
-    if (tid == 0) {
-      double v = 0.0;
-      for (int i = 0; i < 8; ++i) v += part[i];
-      p.logits[(int64_t)t * p.E + e] = v;
-    }
-    __syncthreads();
+  for (int i = 0; i < PER; ++i)
+    if (i * 32 + lane < p.E) sum += (double)expf((float)(v[i] - top));
+  sum = warp_sum(sum);
+  const double w = lane < p.top_k ? (double)expf((float)(mine - top)) / sum : 0.0;
+  const double chosen = p.renorm ? warp_sum(w) : 1.0;
+  if (lane < p.top_k) {
+    sc.ids[t * p.top_k + lane] = my_id;
+    sc.wts[t * p.top_k + lane] = (float)(w / chosen);
   }
-  // the last block to arrive chooses and builds the lists
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) last = atomicInc(&p.lists->arrived, gridDim.x * gridDim.y - 1) == gridDim.x * gridDim.y - 1;
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  for (int t = warp; t < p.T; t += 8) moe_choose(p, t, lane);
-  __syncthreads();
-  moe_build_lists(p, sh, p.ids, p.wts);
 }
 
-__global__ void __launch_bounds__(MOE_THREADS) moe_lists_kernel(const MoeParams p) {
-  __shared__ MoeShared sh;
-  wait_for_previous_kernel();
-  allow_dependent_launch();
-  moe_build_lists(p, sh, p.ids_in, p.wts_in);
+// The choices of all tokens and the lists, by one CTA.
+__device__ __forceinline__ void moe_route(const MoeParams& p, const MoeLists& l, char* scratch, int* warp_sums) {
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, pairs = p.T * p.top_k;
+  const MoeScratch sc(scratch, p.E, pairs);
+  if (p.wr) {
+    for (int t = warp; t < p.T; t += MOE_WARPS) {
+      if (p.E <= 32) moe_choose<1>(p, sc, t, lane);
+      else if (p.E <= 128) moe_choose<4>(p, sc, t, lane);
+      else if (p.E <= 256) moe_choose<8>(p, sc, t, lane);
+      else moe_choose<MOE_MAX_E / 32>(p, sc, t, lane);
+    }
+    if (blockIdx.x == 0) {
+      __syncthreads();
+      for (int i = tid; i < pairs; i += MOE_EXPERT_THREADS) {
+        p.ids[i] = sc.ids[i];
+        p.wts[i] = sc.wts[i];
+      }
+    }
+  } else {
+    for (int i = tid; i < pairs; i += MOE_EXPERT_THREADS) {
+      sc.ids[i] = p.ids_in[i];
+      sc.wts[i] = p.wts_in[i];
+    }
+  }
+  __syncthreads();
+  moe_build_lists(p, l, sc, warp_sums);
 }
 
 // binary32 x as three bf16 planes.
@@ -283,61 +313,62 @@ __global__ void __launch_bounds__(256) moe_split_kernel(const MoeParams p) {
 }
 
 // ---------------------------------------------------------------------------- experts
-constexpr int MOE_DEPTH = 3;   // slots of a warp's ring
-constexpr int MOE_WARPS = 16;  // of an expert kernel's CTA
-constexpr int MOE_EXPERT_THREADS = 32 * MOE_WARPS;
-constexpr int MOE_NT = MOE_ENTRY / 8;
-
 // The 8 values at k of a row of x or h (shared or global memory); zeros past its end.
 __device__ __forceinline__ uint4 moe_row8(const char* row, int k, int K) {
   return k < K ? *reinterpret_cast<const uint4*>(row + k * 2) : make_uint4(0, 0, 0, 0);
 }
 
-// One unit for an entry of `count` tokens: as many column tiles as they need.
-template <int S, int GW, bool ASYM>
-__device__ __forceinline__ void moe_mac(float (&acc)[MOE_NT][4], uint32_t slot, int lane, int count,
-                                        const char* const (&rows)[MOE_NT], int64_t plane, int b, int K) {
+// One unit for an entry of `count` <= 8 NTM tokens: as many column tiles as they need.
+template <int S, int GW, bool ASYM, int NTM>
+__device__ __forceinline__ void moe_mac(float (&acc)[NTM][4], uint32_t slot, int lane, int count,
+                                        const char* const (&rows)[NTM], int64_t plane, int b, int K) {
   const int k0 = b * W4_UNIT + (lane % 4) * 8;
   auto x = [&](int n, int s, int i) { return moe_row8(rows[n] + s * plane, k0 + 32 * i, K); };
-  if (count <= 8) w4_mac<1, S, GW, ASYM>(acc, slot, lane, x);
-  else if (count <= 16) w4_mac<2, S, GW, ASYM>(acc, slot, lane, x);
-  else w4_mac<4, S, GW, ASYM>(acc, slot, lane, x);
+  if (NTM == 1 || count <= 8) w4_mac<1, S, GW, ASYM>(acc, slot, lane, x);
+  else if (count <= 16) w4_mac<(NTM > 1 ? 2 : 1), S, GW, ASYM>(acc, slot, lane, x);
+  else w4_mac<NTM, S, GW, ASYM>(acc, slot, lane, x);
 }
 
 // Gate and up: a tile is 8 rows f of an entry's gate and the same 8 of its up projection, as the two
 // halves of a 16-row tile, so one thread finds both sums of an h.  The tiles of all entries are one
 // line, cut over the CTAs and there over the warps (sq_w4.cuh).
-template <int S, int SH, int GW, bool ASYM>
+template <int NTM, int S, int SH, int GW, bool ASYM>
 __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_up_kernel(const MoeParams p) {
   constexpr int SLOT = W4Slot<GW, ASYM>::BYTES, RP = W4_RP;
   extern __shared__ __align__(16) char smem[];
   __shared__ W4Runs<MOE_WARPS> runs;
+  __shared__ int warp_sums[MOE_WARPS];
   const int tid = threadIdx.x, lane = tid % 32, g = lane / 4, t = lane % 4;
   const int warp = __shfl_sync(0xffffffffu, tid / 32, 0);
   const int cell_floats = min(p.T, MOE_ENTRY) * RP;
   float* cells = reinterpret_cast<float*>(smem + p.up_cells_at);
   const uint32_t ring = smem_u32(smem + p.up_ring_at) + warp * MOE_DEPTH * SLOT;
   const int nb = w4_units(p.D), per_expert = p.F / 8;
+  const int spitch = (int)w4_blocks(p.D) * 256 + 64;  // rows 64 bytes apart modulo 128
+  char* xs = smem + p.up_x_at;
+  const int slots = p.T * p.top_k;
+  const MoeLists l(reinterpret_cast<int*>(smem), p.entries, slots);
   wait_for_previous_kernel();
   allow_dependent_launch();
-  const int64_t tiles = (int64_t)p.lists->active * per_expert;
-  const int64_t t0 = tiles * blockIdx.x / gridDim.x;
-  const int my_tiles = (int)(tiles * (blockIdx.x + 1) / gridDim.x - t0);
+  if (p.x_staged && S == 1) {
+    for (int m = 0; m < p.T; ++m)
+      for (int v = tid; v < p.D / 8; v += MOE_EXPERT_THREADS)
+        cp_async16(smem_u32(xs + m * spitch + v * 16), p.x + m * p.ldx_bytes + v * 16);
+  }
+  cp_commit();
+  moe_route(p, l, smem + p.up_ring_at, warp_sums);
+  if (blockIdx.x == 0)  // for the down kernel
+    for (int i = tid; i < MoeLists::ints(p.entries, slots); i += MOE_EXPERT_THREADS)
+      p.lists[i] = reinterpret_cast<const int*>(smem)[i];
+  const uint32_t tiles = (uint32_t)*l.active * per_expert;
+  const int64_t t0 = w4_part(blockIdx.x, tiles / gridDim.x, tiles % gridDim.x);
+  const int my_tiles = tiles / gridDim.x + (blockIdx.x < tiles % gridDim.x);
   const char* xbase = S == 1 ? p.x : reinterpret_cast<const char*>(p.xparts);
   const int64_t xpitch = S == 1 ? p.ldx_bytes : (int64_t)p.D * 2;
   const int64_t xplane = S == 1 ? 0 : (int64_t)p.T * p.D * 2;
-  const int spitch = (int)w4_blocks(p.D) * 256 + 64;  // rows 64 bytes apart modulo 128
-
   for (int p0 = 0; p0 < my_tiles; p0 += p.up_pass) {
     const int n_tiles = min(p.up_pass, my_tiles - p0), line = n_tiles * nb;
-    if (p0 != 0) __syncthreads();  // the last pass's cells have been read
-    else if (p.x_staged) {
-      for (int m = 0; m < S * p.T; ++m) {
-        const char* src = xbase + (m % p.T) * xpitch + m / p.T * xplane;
-        for (int v = tid; v < p.D / 8; v += MOE_EXPERT_THREADS) cp_async16(smem_u32(smem + m * spitch + v * 16), src + v * 16);
-      }
-    }
-    cp_commit();
+    __syncthreads();  // the last pass's cells have been read, and the route's scratch, where the rings are
     const W4Run run = w4_runs<MOE_WARPS>(runs, line, nb, warp, lane);
     int tile = run.tile, b = run.b;
     float* cell = cells + run.cell * cell_floats + g;
@@ -349,7 +380,7 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_up_kernel(const Moe
     auto place = [&](int ti, int at_b) {
       const int64_t at = t0 + p0 + ti;
       const int a = (int)(at / per_expert), f0 = (int)(at - (int64_t)a * per_expert) * 8;
-      const int64_t e = p.expert[a];
+      const int64_t e = l.expert[a];
       base.codes = p.w13 + e * 2 * p.F * p.rb13;
       base.scales = p.s13 + e * p.g13 * 2 * p.F;
       if (ASYM) base.zeros = p.z13 + e * p.g13 * 2 * p.F;
@@ -373,22 +404,39 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_up_kernel(const Moe
     };
 #pragma unroll 1
     for (int u = 0; u < MOE_DEPTH - 1; ++u) issue(ring + u * SLOT);
-    cp_wait<MOE_DEPTH - 1>();  // x; the ring's blocks are younger
+    if (S > 1 && p.x_staged && p0 == 0) {
+      for (int m = 0; m < p.T; ++m) {
+        const float* src = reinterpret_cast<const float*>(p.x + m * p.ldx_bytes);
+        for (int v = tid; v < p.D / 8; v += MOE_EXPERT_THREADS) {
+          float f[8];
+          load8<false>(reinterpret_cast<const char*>(src + v * 8), f);
+          uint32_t part[8][S];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) split_bf16<S>(f[e], part[e]);
+#pragma unroll
+          for (int s = 0; s < S; ++s)
+            *reinterpret_cast<uint4*>(xs + (s * p.T + m) * spitch + v * 16) =
+                make_uint4(part[0][s] | (part[1][s] << 16), part[2][s] | (part[3][s] << 16),
+                           part[4][s] | (part[5][s] << 16), part[6][s] | (part[7][s] << 16));
+        }
+      }
+    }
+    cp_wait<MOE_DEPTH - 1>();  // x; the ring's units are younger
     __syncthreads();
 
-    float acc[MOE_NT][4] = {};
-    const char* rows[MOE_NT];
+    float acc[NTM][4] = {};
+    const char* rows[NTM];
     int count = 0;
     bool begin = true;
     uint32_t slot = ring, spent = ring + (MOE_DEPTH - 1) * SLOT;
     for (int left = run.units; left > 0; --left) {
       if (begin) {
-        const int a = (int)((t0 + p0 + tile) / per_expert), s0 = p.start[a];
-        count = p.start[a + 1] - s0;
+        const int a = (int)((t0 + p0 + tile) / per_expert), s0 = l.start[a];
+        count = l.start[a + 1] - s0;
 #pragma unroll
-        for (int n = 0; n < MOE_NT; ++n) {
-          const int tok = p.slot_token[s0 + min(8 * n + g, count - 1)];
-          rows[n] = p.x_staged ? smem + tok * spitch : xbase + tok * xpitch;
+        for (int n = 0; n < NTM; ++n) {
+          const int tok = l.token[s0 + min(8 * n + g, count - 1)];
+          rows[n] = p.x_staged ? xs + tok * spitch : xbase + tok * xpitch;
         }
         begin = false;
       }
@@ -400,7 +448,7 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_up_kernel(const Moe
       slot = slot == ring + (MOE_DEPTH - 1) * SLOT ? ring : slot + SLOT;
       if (++b == nb || left == 1) {
 #pragma unroll
-        for (int n = 0; n < MOE_NT; ++n) {
+        for (int n = 0; n < NTM; ++n) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int m = 8 * n + 2 * t + c;
@@ -423,8 +471,8 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_up_kernel(const Moe
     for (int o = tid; o < n_tiles * cols * 8; o += MOE_EXPERT_THREADS) {
       const int f = o % 8, mt = o / 8, ti = mt / cols, m = mt - ti * cols;
       const int64_t at = t0 + p0 + ti;
-      const int a = (int)(at / per_expert), s0 = p.start[a];
-      if (m >= p.start[a + 1] - s0) continue;
+      const int a = (int)(at / per_expert), s0 = l.start[a];
+      if (m >= l.start[a + 1] - s0) continue;
       const float* q = cells + m * RP + f;
       float gate = 0.0f, up = 0.0f;
       const int from = w4_first_cell<MOE_WARPS>(runs, ti, n_tiles, line, inv_line, nb);
@@ -447,7 +495,7 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_up_kernel(const Moe
 // Down: a tile is 16 rows d; its blocks are those of every entry in turn (a rank of a cluster takes
 // a share of that line, where there are few tiles).  A cell holds sums for every token, to which an
 // entry's are added with the tokens' weights when the warp leaves the entry.
-template <int SH, int GW, bool ASYM>
+template <int NTM, int SH, int GW, bool ASYM>
 __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_down_kernel(const MoeParams p) {
   constexpr int SLOT = W4Slot<GW, ASYM>::BYTES, RP = W4_RP;
   extern __shared__ __align__(16) char smem[];
@@ -455,7 +503,7 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_down_kernel(const M
   const int tid = threadIdx.x, lane = tid % 32, g = lane / 4, t = lane % 4;
   const int warp = __shfl_sync(0xffffffffu, tid / 32, 0);
   const int cell_floats = p.T * RP;
-  float* cells = reinterpret_cast<float*>(smem);
+  float* cells = reinterpret_cast<float*>(smem + p.down_cells_at);
   const uint32_t ring = smem_u32(smem + p.down_ring_at) + warp * MOE_DEPTH * SLOT;
   float* out = reinterpret_cast<float*>(smem + p.down_ring_at);  // [tile][token][row] over the ranks, after the rings
   const int nb = w4_units(p.F);
@@ -464,7 +512,12 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_down_kernel(const M
   const int my_tiles = (int)((int64_t)tiles * (cluster + 1) / clusters) - t0;
   wait_for_previous_kernel();
   allow_dependent_launch();
-  const int all = p.lists->active * nb, first = (int)((int64_t)all * rank / p.C);
+  const int slots = p.T * p.top_k;
+  const MoeLists l(reinterpret_cast<int*>(smem), p.entries, slots);
+  for (int i = tid; i < MoeLists::ints(p.entries, slots); i += MOE_EXPERT_THREADS)
+    reinterpret_cast<int*>(smem)[i] = p.lists[i];
+  __syncthreads();
+  const int all = *l.active * nb, first = (int)((int64_t)all * rank / p.C);
   const int per_tile = (int)((int64_t)all * (rank + 1) / p.C) - first;
   const int64_t plane = (int64_t)p.T * p.top_k * p.F * 2;
 
@@ -482,7 +535,7 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_down_kernel(const M
       base.pitch = p.D;
       base.groups = p.g2;
         auto place = [&](int ti, int entry, int at_b) {
-        const int64_t e = p.expert[entry];
+        const int64_t e = l.expert[entry];
         base.codes = p.w2 + e * p.D * p.rb2;
         base.scales = p.s2 + e * p.g2 * p.D;
         if (ASYM) base.zeros = p.z2 + e * p.g2 * p.D;
@@ -515,8 +568,8 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_down_kernel(const M
 #pragma unroll 1
       for (int u = 0; u < MOE_DEPTH - 1; ++u) issue(ring + u * SLOT);
 
-      float acc[MOE_NT][4] = {};
-      const char* rows[MOE_NT];
+      float acc[NTM][4] = {};
+      const char* rows[NTM];
       int s0 = 0, count = 0;
       bool begin = true, fresh = true;
       uint32_t slot = ring, spent = ring + (MOE_DEPTH - 1) * SLOT;
@@ -527,10 +580,10 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_down_kernel(const M
           fresh = false;
         }
         if (begin) {
-          s0 = p.start[a];
-          count = p.start[a + 1] - s0;
+          s0 = l.start[a];
+          count = l.start[a + 1] - s0;
 #pragma unroll
-          for (int n = 0; n < MOE_NT; ++n)
+          for (int n = 0; n < NTM; ++n)
             rows[n] = reinterpret_cast<const char*>(p.h + (int64_t)(s0 + min(8 * n + g, count - 1)) * p.F);
           begin = false;
         }
@@ -543,13 +596,13 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_down_kernel(const M
         ++at;
         if (++b == nb || at == per_tile || left == 1) {
 #pragma unroll
-          for (int n = 0; n < MOE_NT; ++n) {
+          for (int n = 0; n < NTM; ++n) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const int m = 8 * n + 2 * t + c;
               if (m < count) {  // an entry's tokens differ, so no two lanes meet in a place
-                const float w = p.slot_weight[s0 + m];
-                float* q = cell + p.slot_token[s0 + m] * RP + g;
+                const float w = l.weight[s0 + m];
+                float* q = cell + l.token[s0 + m] * RP + g;
                 q[0] = __fmaf_rn(w, acc[n][c], q[0]);
                 q[8] = __fmaf_rn(w, acc[n][2 + c], q[8]);
               }
@@ -624,12 +677,14 @@ cudaError_t launch_dependent(const void* kern, unsigned gx, unsigned gy, unsigne
   return cudaLaunchKernelExC(&cfg, kern, args);
 }
 
+int64_t up16(int64_t v) { return (v + 15) & ~(int64_t)15; }
+
 constexpr int64_t kSmemBudget = 226 * 1024;  // of 227 KB; the rest covers the static arrays
 
-template <int S, int SH, int GW, bool ASYM>
-cudaError_t launch_experts(sqk::MoeParams p, cudaStream_t st) {
-  const void* up = (const void*)sqk::moe_up_kernel<S, SH, GW, ASYM>;
-  const void* down = (const void*)sqk::moe_down_kernel<SH, GW, ASYM>;
+template <int NTM, int S, int SH, int GW, bool ASYM>
+cudaError_t launch_experts_t(sqk::MoeParams p, cudaStream_t st) {
+  const void* up = (const void*)sqk::moe_up_kernel<NTM, S, SH, GW, ASYM>;
+  const void* down = (const void*)sqk::moe_down_kernel<NTM, SH, GW, ASYM>;
   for (const void* k : {up, down}) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBudget);
     if (e != cudaSuccess) return e;
@@ -642,11 +697,19 @@ cudaError_t launch_experts(sqk::MoeParams p, cudaStream_t st) {
   const int64_t cell = (int64_t)std::min(p.T, sqk::MOE_ENTRY) * sqk::W4_RP * 4;
   const int64_t x = (int64_t)S * p.T * (sqk::w4_blocks(p.D) * 256 + 64);
   auto passes = [&](int64_t room, int64_t c, int64_t n) { return std::min(n, room / c - (sqk::MOE_WARPS - 1)); };
-  p.x_staged = passes(kSmemBudget - ring - x, cell, per) >= std::min<int64_t>(per, std::max<int64_t>(8, per / 2));
-  p.up_cells_at = p.x_staged ? (int)x : 0;
-  p.up_pass = (int)passes(kSmemBudget - ring - p.up_cells_at, cell, per);
+  const int64_t slots = (int64_t)p.T * p.top_k, lists = up16(sqk::MoeLists::ints(p.entries, slots) * 4);
+  const int64_t rings = std::max(ring, sqk::MoeScratch::bytes(p.E, slots));  // the route's scratch comes before
+  p.x_staged = passes(kSmemBudget - lists - rings - x, cell, per) >= std::min<int64_t>(per, std::max<int64_t>(8, per / 2));
+  p.up_x_at = (int)lists;
+  p.up_cells_at = (int)(lists + (p.x_staged ? x : 0));
+  p.up_pass = (int)passes(kSmemBudget - rings - p.up_cells_at, cell, per);
   p.up_ring_at = (int)(p.up_cells_at + (p.up_pass + sqk::MOE_WARPS - 1) * cell);
-  cudaError_t e = launch_dependent(up, (unsigned)sms, 1, sqk::MOE_EXPERT_THREADS, (size_t)(p.up_ring_at + ring), 1, p, st);
+  cudaError_t e = cudaSuccess;
+  if (S > 1 && !p.x_staged) {
+    e = launch_dependent((const void*)sqk::moe_split_kernel, (unsigned)sms, 1, 256, 0, 1, p, st);
+    if (e != cudaSuccess) return e;
+  }
+  e = launch_dependent(up, (unsigned)sms, 1, sqk::MOE_EXPERT_THREADS, (size_t)(p.up_ring_at + rings), 1, p, st);
   if (e != cudaSuccess) return e;
 
   const int64_t tiles = (p.D + 15) / 16, cell2 = (int64_t)p.T * sqk::W4_RP * 4;
@@ -671,10 +734,17 @@ cudaError_t launch_experts(sqk::MoeParams p, cudaStream_t st) {
   }
   const int64_t per2 = (tiles + clusters - 1) / clusters;
   // the sums over the ranks take the rings' place
-  p.down_pass = (int)std::min(passes(kSmemBudget - ring, cell2, per2), std::max<int64_t>(1, ring / ((int64_t)p.T * 64)));
-  p.down_ring_at = (int)((p.down_pass + sqk::MOE_WARPS - 1) * cell2);
+  p.down_pass = (int)std::min(passes(kSmemBudget - lists - ring, cell2, per2), std::max<int64_t>(1, ring / ((int64_t)p.T * 64)));
+  p.down_cells_at = (int)lists;
+  p.down_ring_at = (int)(lists + (p.down_pass + sqk::MOE_WARPS - 1) * cell2);
   return launch_dependent(down, (unsigned)(clusters * p.C), 1, sqk::MOE_EXPERT_THREADS, (size_t)(p.down_ring_at + ring), p.C, p,
                           st);
+}
+
+template <int S, int SH, int GW, bool ASYM>
+cudaError_t launch_experts(const sqk::MoeParams& p, cudaStream_t st) {
+  return p.T <= 8 ? launch_experts_t<1, S, SH, GW, ASYM>(p, st)
+                  : launch_experts_t<sqk::MOE_ENTRY / 8, S, SH, GW, ASYM>(p, st);
 }
 
 template <int S, int SH>
@@ -702,22 +772,16 @@ static size_t moe_layout(sqk::MoeParams* p, char* base, int64_t T, int64_t D, in
     return r;
   };
   sqk::MoeParams q{};
-  q.lists = (sqk::MoeLists*)take(sizeof(sqk::MoeLists));
+  // every expert's last entry may be short
+  q.entries = (int)std::min(T * k, E + T * k / sqk::MOE_ENTRY);
   q.logits = (double*)take((size_t)(T * E) * 8);
-  const int64_t entries = std::min(T * k, E + T * k / sqk::MOE_ENTRY);  // every expert's last one may be short
-  q.expert = (int*)take((size_t)entries * 4);
-  q.start = (int*)take((size_t)(entries + 1) * 4);
-  q.slot_token = (int*)take((size_t)(T * k) * 4);
-  q.slot_weight = (float*)take((size_t)(T * k) * 4);
+  q.lists = (int*)take((size_t)sqk::MoeLists::ints(q.entries, T * k) * 4);
   q.xparts = (uint16_t*)take((size_t)(3 * T * D) * 2);
   q.h = (uint16_t*)take((size_t)(3 * T * k * F) * 2);
   if (p) {
-    p->lists = q.lists;
+    p->entries = q.entries;
     p->logits = q.logits;
-    p->expert = q.expert;
-    p->start = q.start;
-    p->slot_token = q.slot_token;
-    p->slot_weight = q.slot_weight;
+    p->lists = q.lists;
     p->xparts = q.xparts;
     p->h = q.h;
   }
@@ -765,19 +829,20 @@ cudaError_t launch_moe_w4(const void* x, bool bf16, int64_t T, int64_t D, int64_
   p.ldy = ldy;
   p.y_bf16 = y_bf16;
   p.C = 1;
-  cudaError_t e;
-  if (!bf16) {
-    e = launch_dependent((const void*)sqk::moe_split_kernel, (unsigned)num_sms(), 1, 256, 0, 1, p, st);
+  if (wr) {
+    // one token: a block per expert; more: blocks of 4 experts and 8 tokens
+    const void* k;
+    if (T == 1)
+      k = bf16 ? (wr_bf16 ? (const void*)sqk::moe_logits_kernel<true, true, 1, 1> : (const void*)sqk::moe_logits_kernel<true, false, 1, 1>)
+               : (wr_bf16 ? (const void*)sqk::moe_logits_kernel<false, true, 1, 1> : (const void*)sqk::moe_logits_kernel<false, false, 1, 1>);
+    else
+      k = bf16 ? (wr_bf16 ? (const void*)sqk::moe_logits_kernel<true, true, 4, 8> : (const void*)sqk::moe_logits_kernel<true, false, 4, 8>)
+               : (wr_bf16 ? (const void*)sqk::moe_logits_kernel<false, true, 4, 8> : (const void*)sqk::moe_logits_kernel<false, false, 4, 8>);
+    const unsigned eb = T == 1 ? 1 : 4, tb = T == 1 ? 1 : 8;
+    const cudaError_t e = launch_dependent(k, ((unsigned)E + eb - 1) / eb, ((unsigned)T + tb - 1) / tb,
+                                           32 * sqk::MOE_LOGIT_WARPS, 0, 1, p, st);
     if (e != cudaSuccess) return e;
   }
-  if (wr) {
-    const void* k = bf16 ? (wr_bf16 ? (const void*)sqk::moe_router_kernel<true, true> : (const void*)sqk::moe_router_kernel<true, false>)
-                         : (wr_bf16 ? (const void*)sqk::moe_router_kernel<false, true> : (const void*)sqk::moe_router_kernel<false, false>);
-    e = launch_dependent(k, (unsigned)E, (unsigned)std::min<int64_t>(T, 8), sqk::MOE_THREADS, 0, 1, p, st);
-  } else {
-    e = launch_dependent((const void*)sqk::moe_lists_kernel, 1, 1, sqk::MOE_THREADS, 0, 1, p, st);
-  }
-  if (e != cudaSuccess) return e;
   return bf16 ? launch_experts_g<1, 2>(p, group, st) : launch_experts_g<3, 3>(p, group, st);
 }
 
