@@ -135,6 +135,23 @@ def test_gemm_sizes(M, K, N, group, asym, dt):
     assert torch.equal(y, sq.sq_w4_gemm(dev(x, dt), wq, sg, zp, group=group, out_dtype=torch.float32))
 
 
+@pytest.mark.parametrize("M", [1, 2, 3, 5, 8])
+@pytest.mark.parametrize("group,asym,dt", [(32, True, "bf16"), (64, False, "bf16"), (128, True, "bf16"), (128, False, "f32"),
+                                           (64, True, "f32"), (32, False, "f32")])
+def test_gemm_many_channels_for_few_tokens(M, group, asym, dt):
+    """Enough tiles for the products in digits; tokens of very different magnitudes, one of them zero."""
+    rng = np.random.default_rng(M + group)
+    K, N = 528, 21008
+    (wq, sg, zp), w = random_weight(rng, K, N, group, asym)
+    x = activations(rng, M, K, dt)
+    x[0] *= np.float32(2.0 ** -90)
+    x[M - 1, 3] *= np.float32(2.0 ** 60)
+    if M > 2:
+        x[1] = 0
+    ref, bound = P.product(x, w, group)
+    check(sq.sq_w4_gemm(dev(x, dt), wq, sg, zp, group=group, out_dtype=torch.float32), ref, bound, "f32")
+
+
 def test_gemm_many_tokens():
     rng = np.random.default_rng(6)
     (wq, sg, zp), w = random_weight(rng, 272, 100, 128, False)
@@ -157,10 +174,11 @@ def test_gemm_strides_and_the_rows_behind():
     assert (y == -7).all()
 
 
-def test_gemm_is_exact_on_integers():
+@pytest.mark.parametrize("M,N", [(6, 77), (6, 19000), (1, 5000), (8, 24000)])
+def test_gemm_is_exact_on_integers(M, N):
     """Small integers in x and power-of-two scales: every sum is exact, so every bit must agree."""
     rng = np.random.default_rng(8)
-    K, N, M = 2064, 77, 6
+    K = 2064 if M == 6 and N == 77 else 304
     codes = rng.integers(0, 16, (N, K)).astype(np.uint8)
     sg = (2.0 ** rng.integers(-3, 4, (-(-K // 64), N))).astype(np.float32)
     zp = rng.integers(0, 16, sg.shape).astype(np.uint8)
@@ -185,10 +203,11 @@ def test_gemm_takes_binary32_inputs_whole():
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_gemm_keeps_infinities_and_nan_in_their_rows(dt):
+@pytest.mark.parametrize("N", [50, 15000])
+def test_gemm_keeps_infinities_and_nan_in_their_rows(N, dt):
     rng = np.random.default_rng(9)
-    (wq, sg, _), _ = random_weight(rng, 400, 50, 128, False)
-    codes = rng.integers(9, 16, (50, 400)).astype(np.uint8)  # positive weights only
+    (wq, sg, _), _ = random_weight(rng, 400, N, 128, False)
+    codes = rng.integers(9, 16, (N, 400)).astype(np.uint8)  # positive weights only
     wq = dev(P.pack(codes))
     w = P.values(P.pack(codes), sg.float().cpu().numpy(), None, 400, 128)
     x = activations(rng, 6, 400, dt)

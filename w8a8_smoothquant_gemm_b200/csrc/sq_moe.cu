@@ -8,13 +8,12 @@
 // programmatic dependents: router logits; choice, gate and up; down.  The work is cut by (expert,
 // rows), never by token: an expert's weights are read once for all of its tokens, which are the
 // columns of the mma (sq_w4.cuh).
-//   Router sums are binary64, so that which experts are chosen does not hang on rounding.  Every CTA
-// of the gate/up kernel makes the choice for itself from the logits (a warp per token, a few hundred
-// cycles), which is shorter than one block doing it for all behind another pair of fences.  h is
-// kept as two bf16 parts (16 significant bits; three for a binary32 layer), so the only bf16
-// rounding of the layer is the final store.  Every sum has a fixed order; the only atomics are the
-// lists' bit masks (order-free).  The expert kernels are one CTA per SM with the weight stream of
-// sq_w4.cuh.
+//   Router sums are binary64, so that which experts are chosen does not hang on rounding.  The last
+// of the blocks that work on a token makes its choice; the lists are short enough that every CTA of the
+// gate/up kernel builds them for itself.  h is kept as two bf16 parts (16 significant bits; three for a
+// binary32 layer), so the only bf16 rounding of the layer is the final store.  Every sum has a fixed
+// order; the only atomics are the lists' bit masks (order-free) and the router's arrival counts.  The
+// expert kernels are one CTA per SM with the weight stream of sq_w4.cuh.
 #include <algorithm>
 
 #include "sq_w4.cuh"
@@ -34,7 +33,7 @@ struct MoeParams {
   int T, D, F, E, top_k, renorm;
   int* ids;
   float* wts;
-  const int* ids_in;
+  const int* ids_in;    // what the experts go by: ids and wts, or choices made elsewhere
   const float* wts_in;
   const char *w13, *w2;
   const uint16_t *s13, *s2;
@@ -45,22 +44,23 @@ struct MoeParams {
   int64_t ldy;
   int y_bf16;
   // workspace
-  double* logits;       // [T, E]
+  unsigned int* arrived;  // [8] router blocks that are done with 8 tokens; wrap to 0 by themselves
+  double* logits;         // [T, E]
   int* lists;           // see MoeLists
   uint16_t* xparts;     // [3, T, D] (binary32 x)
   uint16_t* h;          // [parts, T k, F]
   // the expert kernels' shared memory
   int entries;          // most entries of the lists
-  bool x_staged;        // x in shared memory
   int up_x_at, up_cells_at, up_ring_at, up_pass;  // the lists come first; pass: tiles whose cells fit
-  int down_cells_at, down_ring_at, down_pass;
+  int down_h_at, down_cells_at, down_ring_at, down_pass;
   int C;                // CTAs of the down kernel's cluster
 };
 
-constexpr int MOE_DEPTH = 3;   // slots of a warp's ring
+constexpr int MOE_DEPTH = 2;   // slots of a warp's ring
 constexpr int MOE_WARPS = 16;  // of an expert kernel's CTA
 constexpr int MOE_EXPERT_THREADS = 32 * MOE_WARPS;
 constexpr int MOE_LOGIT_WARPS = 8;
+constexpr int MOE_RP = 20;  // floats between the down kernel's tokens of a cell: 16 rows, padded to spread the banks
 
 // ---------------------------------------------------------------------------- lists
 // Entries (an expert and up to MOE_ENTRY of its tokens), and slots (a token of an expert), which lie
@@ -175,57 +175,15 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
-// Logits of EB experts and TB tokens by one block, its 8 warps and their lanes along D.  Bound by the
-// conversions to binary64 (EB + TB of them for EB TB multiply-adds).
-template <bool XB, bool RB, int EB, int TB>
-__global__ void __launch_bounds__(32 * MOE_LOGIT_WARPS) moe_logits_kernel(const MoeParams p) {
-  __shared__ double part[MOE_LOGIT_WARPS][EB * TB];
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int e0 = blockIdx.x * EB, t0 = blockIdx.y * TB;
-  wait_for_previous_kernel();
-  allow_dependent_launch();
-  double sum[EB][TB] = {};
-  for (int d = tid * 8; d < p.D; d += MOE_LOGIT_WARPS * 256) {
-    float w[EB][8];
-#pragma unroll
-    for (int e = 0; e < EB; ++e)  // experts and tokens past the end repeat the last one, not stored
-      load8<RB>(p.wr + ((int64_t)min(e0 + e, p.E - 1) * p.D + d) * (RB ? 2 : 4), w[e]);
-#pragma unroll
-    for (int t = 0; t < TB; ++t) {
-      float x[8];
-      load8<XB>(p.x + min(t0 + t, p.T - 1) * p.ldx_bytes + (int64_t)d * (XB ? 2 : 4), x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int e = 0; e < EB; ++e) sum[e][t] = fma((double)x[i], (double)w[e][i], sum[e][t]);
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < EB; ++e)
-#pragma unroll
-    for (int t = 0; t < TB; ++t) {
-      const double v = warp_sum(sum[e][t]);
-      if (lane == 0) part[warp][e * TB + t] = v;
-    }
-  __syncthreads();
-  if (tid < EB * TB) {
-    double v = part[0][tid];
-#pragma unroll
-    for (int i = 1; i < MOE_LOGIT_WARPS; ++i) v += part[i][tid];
-    const int e = e0 + tid / TB, t = t0 + tid % TB;
-    if (e < p.E && t < p.T) p.logits[(int64_t)t * p.E + e] = v;
-  }
-}
-
 // The k largest logits of one token, by one warp, PER of them a lane: ties to the lowest index, NaN
 // ranks last.  Compared as integers of the same order (0: none, 1: NaN).
 template <int PER>
-__device__ __noinline__ void moe_choose(const MoeParams& p, const MoeScratch& sc, int t, int lane) {
+__device__ void moe_choose(const MoeParams& p, int t, int lane) {
   const double* row = p.logits + (int64_t)t * p.E;
   double v[PER];
   unsigned long long key[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) v[i] = i * 32 + lane < p.E ? row[i * 32 + lane] : 0.0;
+  for (int i = 0; i < PER; ++i) v[i] = i * 32 + lane < p.E ? __ldcg(row + i * 32 + lane) : 0.0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const unsigned long long b = (unsigned long long)__double_as_longlong(v[i]);
@@ -265,36 +223,73 @@ __device__ __noinline__ void moe_choose(const MoeParams& p, const MoeScratch& sc
   const double w = lane < p.top_k ? (double)expf((float)(mine - top)) / sum : 0.0;
   const double chosen = p.renorm ? warp_sum(w) : 1.0;
   if (lane < p.top_k) {
-    sc.ids[t * p.top_k + lane] = my_id;
-    sc.wts[t * p.top_k + lane] = (float)(w / chosen);
+    p.ids[t * p.top_k + lane] = my_id;
+    p.wts[t * p.top_k + lane] = (float)(w / chosen);
   }
 }
 
-// The choices of all tokens and the lists, by one CTA.
-__device__ __forceinline__ void moe_route(const MoeParams& p, const MoeLists& l, char* scratch, int* warp_sums) {
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, pairs = p.T * p.top_k;
-  const MoeScratch sc(scratch, p.E, pairs);
-  if (p.wr) {
-    for (int t = warp; t < p.T; t += MOE_WARPS) {
-      if (p.E <= 32) moe_choose<1>(p, sc, t, lane);
-      else if (p.E <= 128) moe_choose<4>(p, sc, t, lane);
-      else if (p.E <= 256) moe_choose<8>(p, sc, t, lane);
-      else moe_choose<MOE_MAX_E / 32>(p, sc, t, lane);
-    }
-    if (blockIdx.x == 0) {
-      __syncthreads();
-      for (int i = tid; i < pairs; i += MOE_EXPERT_THREADS) {
-        p.ids[i] = sc.ids[i];
-        p.wts[i] = sc.wts[i];
-      }
-    }
-  } else {
-    for (int i = tid; i < pairs; i += MOE_EXPERT_THREADS) {
-      sc.ids[i] = p.ids_in[i];
-      sc.wts[i] = p.wts_in[i];
+// Logits of EB experts and TB tokens by one block, its 8 warps and their lanes along D.  Bound by the
+// conversions to binary64 (EB + TB of them for EB TB multiply-adds).  The last block to arrive for its
+// tokens makes their choices, a warp each.
+template <bool XB, bool RB, int EB, int TB>
+__global__ void __launch_bounds__(32 * MOE_LOGIT_WARPS) moe_logits_kernel(const MoeParams p) {
+  __shared__ double part[MOE_LOGIT_WARPS][EB * TB];
+  __shared__ bool last;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int e0 = blockIdx.x * EB, t0 = blockIdx.y * TB;
+  wait_for_previous_kernel();
+  allow_dependent_launch();
+  double sum[EB][TB] = {};
+  for (int d = tid * 8; d < p.D; d += MOE_LOGIT_WARPS * 256) {
+    float w[EB][8];
+#pragma unroll
+    for (int e = 0; e < EB; ++e)  // experts and tokens past the end repeat the last one, not stored
+      load8<RB>(p.wr + ((int64_t)min(e0 + e, p.E - 1) * p.D + d) * (RB ? 2 : 4), w[e]);
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+      float x[8];
+      load8<XB>(p.x + min(t0 + t, p.T - 1) * p.ldx_bytes + (int64_t)d * (XB ? 2 : 4), x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < EB; ++e) sum[e][t] = fma((double)x[i], (double)w[e][i], sum[e][t]);
     }
   }
+#pragma unroll
+  for (int e = 0; e < EB; ++e)
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+      const double v = warp_sum(sum[e][t]);
+      if (lane == 0) part[warp][e * TB + t] = v;
+    }
   __syncthreads();
+  if (tid < EB * TB) {
+    double v = part[0][tid];
+#pragma unroll
+    for (int i = 1; i < MOE_LOGIT_WARPS; ++i) v += part[i][tid];
+    const int e = e0 + tid / TB, t = t0 + tid % TB;
+    if (e < p.E && t < p.T) p.logits[(int64_t)t * p.E + e] = v;
+    __threadfence();
+  }
+  __syncthreads();
+  if (tid == 0) last = atomicInc(p.arrived + blockIdx.y, gridDim.x - 1) == gridDim.x - 1;
+  __syncthreads();
+  if (!last || warp >= TB || t0 + warp >= p.T) return;
+  __threadfence();
+  if (p.E <= 32) moe_choose<1>(p, t0 + warp, lane);
+  else if (p.E <= 128) moe_choose<4>(p, t0 + warp, lane);
+  else if (p.E <= 256) moe_choose<8>(p, t0 + warp, lane);
+  else moe_choose<MOE_MAX_E / 32>(p, t0 + warp, lane);
+}
+
+// The lists, by one CTA, from the choices in global memory.
+__device__ __forceinline__ void moe_route(const MoeParams& p, const MoeLists& l, char* scratch, int* warp_sums) {
+  const int pairs = p.T * p.top_k;
+  const MoeScratch sc(scratch, p.E, pairs);
+  for (int i = threadIdx.x; i < pairs; i += MOE_EXPERT_THREADS) {
+    sc.ids[i] = p.ids_in[i];
+    sc.wts[i] = p.wts_in[i];
+  }
   moe_build_lists(p, l, sc, warp_sums);
 }
 
@@ -313,48 +308,69 @@ __global__ void __launch_bounds__(256) moe_split_kernel(const MoeParams p) {
 }
 
 // ---------------------------------------------------------------------------- experts
-// The 8 values at k of a row of x or h (shared or global memory); zeros past its end.
-__device__ __forceinline__ uint4 moe_row8(const char* row, int k, int K) {
-  return k < K ? *reinterpret_cast<const uint4*>(row + k * 2) : make_uint4(0, 0, 0, 0);
-}
-
-// One unit for an entry of `count` <= 8 NTM tokens: as many column tiles as they need.
-template <int S, int GW, bool ASYM, int NTM>
+// One unit for an entry of `count` <= 8 NTM tokens: as many column tiles as they need.  STAGED: rows are
+// addresses in shared memory, padded with zeros to whole units; else they are read past the caches' help
+// from global memory, `K` values of them.
+template <bool STAGED, int S, int GW, bool ASYM, int NTM, typename Row>
 __device__ __forceinline__ void moe_mac(float (&acc)[NTM][4], uint32_t slot, int lane, int count,
-                                        const char* const (&rows)[NTM], int64_t plane, int b, int K) {
-  const int k0 = b * W4_UNIT + (lane % 4) * 8;
-  auto x = [&](int n, int s, int i) { return moe_row8(rows[n] + s * plane, k0 + 32 * i, K); };
+                                        const Row (&rows)[NTM], int64_t plane, int u, int K) {
+  auto x = [&](int n, int s, int i) {
+    if constexpr (STAGED) {
+      return lds128(rows[n] + s * (uint32_t)plane + u * (2 * W4_UNIT) + i * 64);
+    } else {
+      const int k = u * W4_UNIT + (lane % 4) * 8 + 32 * i;
+      return k < K ? *reinterpret_cast<const uint4*>(rows[n] + s * plane + k * 2) : make_uint4(0, 0, 0, 0);
+    }
+  };
   if (NTM == 1 || count <= 8) w4_mac<1, S, GW, ASYM>(acc, slot, lane, x);
   else if (count <= 16) w4_mac<(NTM > 1 ? 2 : 1), S, GW, ASYM>(acc, slot, lane, x);
   else w4_mac<NTM, S, GW, ASYM>(acc, slot, lane, x);
 }
 
+template <bool STAGED>
+struct MoeRow {
+  using type = const char*;
+  static __device__ __forceinline__ type of(uint32_t, const char* global, int) { return global; }
+};
+template <>
+struct MoeRow<true> {
+  using type = uint32_t;
+  static __device__ __forceinline__ type of(uint32_t shared, const char*, int lane) { return shared + (lane % 4) * 16; }
+};
+
+// Bytes between staged rows of K bf16 numbers: whole units, rows 64 bytes apart modulo 128.
+__host__ __device__ __forceinline__ int moe_row_pitch(int K) { return w4_units(K) * (2 * W4_UNIT) + 64; }
+
+// Starts the copies of a row of K bf16 numbers to shared memory, with zeros up to whole units.
+__device__ __forceinline__ void moe_stage_row(char* dst, const char* src, int K) {
+  for (int v = threadIdx.x; v < w4_units(K) * (W4_UNIT / 8); v += MOE_EXPERT_THREADS) {
+    if (v * 8 < K) cp_async16(smem_u32(dst + v * 16), src + v * 16);
+    else *reinterpret_cast<uint4*>(dst + v * 16) = make_uint4(0, 0, 0, 0);
+  }
+}
+
 // Gate and up: a tile is 8 rows f of an entry's gate and the same 8 of its up projection, as the two
 // halves of a 16-row tile, so one thread finds both sums of an h.  The tiles of all entries are one
 // line, cut over the CTAs and there over the warps (sq_w4.cuh).
-template <int NTM, int S, int SH, int GW, bool ASYM>
+template <bool STAGED, int NTM, int S, int SH, int GW, bool ASYM>
 __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_up_kernel(const MoeParams p) {
-  constexpr int SLOT = W4Slot<GW, ASYM>::BYTES, RP = W4_RP;
+  constexpr int SLOT = W4Slot<GW, ASYM>::BYTES, CELL = w4_cell_floats(NTM);
   extern __shared__ __align__(16) char smem[];
   __shared__ W4Runs<MOE_WARPS> runs;
   __shared__ int warp_sums[MOE_WARPS];
   const int tid = threadIdx.x, lane = tid % 32, g = lane / 4, t = lane % 4;
   const int warp = __shfl_sync(0xffffffffu, tid / 32, 0);
-  const int cell_floats = min(p.T, MOE_ENTRY) * RP;
   float* cells = reinterpret_cast<float*>(smem + p.up_cells_at);
   const uint32_t ring = smem_u32(smem + p.up_ring_at) + warp * MOE_DEPTH * SLOT;
   const int nb = w4_units(p.D), per_expert = p.F / 8;
-  const int spitch = (int)w4_blocks(p.D) * 256 + 64;  // rows 64 bytes apart modulo 128
+  const int spitch = moe_row_pitch(p.D);
   char* xs = smem + p.up_x_at;
   const int slots = p.T * p.top_k;
   const MoeLists l(reinterpret_cast<int*>(smem), p.entries, slots);
   wait_for_previous_kernel();
   allow_dependent_launch();
-  if (p.x_staged && S == 1) {
-    for (int m = 0; m < p.T; ++m)
-      for (int v = tid; v < p.D / 8; v += MOE_EXPERT_THREADS)
-        cp_async16(smem_u32(xs + m * spitch + v * 16), p.x + m * p.ldx_bytes + v * 16);
-  }
+  if (STAGED && S == 1)
+    for (int m = 0; m < p.T; ++m) moe_stage_row(xs + m * spitch, p.x + m * p.ldx_bytes, p.D);
   cp_commit();
   moe_route(p, l, smem + p.up_ring_at, warp_sums);
   if (blockIdx.x == 0)  // for the down kernel
@@ -371,15 +387,15 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_up_kernel(const Moe
     __syncthreads();  // the last pass's cells have been read, and the route's scratch, where the rings are
     const W4Run run = w4_runs<MOE_WARPS>(runs, line, nb, warp, lane);
     int tile = run.tile, b = run.b;
-    float* cell = cells + run.cell * cell_floats + g;
+    float* cell = cells + run.cell * CELL;
 
     W4Base base{};
     base.row_bytes = (uint32_t)p.rb13;
     base.pitch = 2 * p.F;
     base.groups = p.g13;
     auto place = [&](int ti, int at_b) {
-      const int64_t at = t0 + p0 + ti;
-      const int a = (int)(at / per_expert), f0 = (int)(at - (int64_t)a * per_expert) * 8;
+      const uint32_t at = (uint32_t)t0 + p0 + ti;  // of the tiles of all entries, below 2^32
+      const int a = (int)(at / (uint32_t)per_expert), f0 = (int)(at - a * per_expert) * 8;
       const int64_t e = l.expert[a];
       base.codes = p.w13 + e * 2 * p.F * p.rb13;
       base.scales = p.s13 + e * p.g13 * 2 * p.F;
@@ -404,12 +420,12 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_up_kernel(const Moe
     };
 #pragma unroll 1
     for (int u = 0; u < MOE_DEPTH - 1; ++u) issue(ring + u * SLOT);
-    if (S > 1 && p.x_staged && p0 == 0) {
+    if (STAGED && S > 1 && p0 == 0) {
       for (int m = 0; m < p.T; ++m) {
         const float* src = reinterpret_cast<const float*>(p.x + m * p.ldx_bytes);
-        for (int v = tid; v < p.D / 8; v += MOE_EXPERT_THREADS) {
-          float f[8];
-          load8<false>(reinterpret_cast<const char*>(src + v * 8), f);
+        for (int v = tid; v < nb * (W4_UNIT / 8); v += MOE_EXPERT_THREADS) {
+          float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+          if (v * 8 < p.D) load8<false>(reinterpret_cast<const char*>(src + v * 8), f);
           uint32_t part[8][S];
 #pragma unroll
           for (int e = 0; e < 8; ++e) split_bf16<S>(f[e], part[e]);
@@ -425,67 +441,58 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_up_kernel(const Moe
     __syncthreads();
 
     float acc[NTM][4] = {};
-    const char* rows[NTM];
+    typename MoeRow<STAGED>::type rows[NTM];
     int count = 0;
     bool begin = true;
     uint32_t slot = ring, spent = ring + (MOE_DEPTH - 1) * SLOT;
     for (int left = run.units; left > 0; --left) {
       if (begin) {
-        const int a = (int)((t0 + p0 + tile) / per_expert), s0 = l.start[a];
+        const int a = (int)(((uint32_t)t0 + p0 + tile) / (uint32_t)per_expert), s0 = l.start[a];
         count = l.start[a + 1] - s0;
 #pragma unroll
         for (int n = 0; n < NTM; ++n) {
           const int tok = l.token[s0 + min(8 * n + g, count - 1)];
-          rows[n] = p.x_staged ? xs + tok * spitch : xbase + tok * xpitch;
+          rows[n] = MoeRow<STAGED>::of(smem_u32(xs) + tok * spitch, xbase + tok * xpitch, lane);
         }
         begin = false;
       }
       cp_wait<MOE_DEPTH - 2>();
       __syncwarp();
       issue(spent);
-      moe_mac<S, GW, ASYM>(acc, slot, lane, count, rows, p.x_staged ? (int64_t)p.T * spitch : xplane, b, p.D);
+      moe_mac<STAGED, S, GW, ASYM>(acc, slot, lane, count, rows, STAGED ? (int64_t)p.T * spitch : xplane, b, p.D);
       spent = slot;
       slot = slot == ring + (MOE_DEPTH - 1) * SLOT ? ring : slot + SLOT;
       if (++b == nb || left == 1) {
+        if (NTM == 1 || count <= 8) w4_put_cell<1>(cell, acc, lane);
+        else w4_put_cell<NTM>(cell, acc, lane);
+        cell += CELL;
 #pragma unroll
-        for (int n = 0; n < NTM; ++n) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int m = 8 * n + 2 * t + c;
-            if (m < count) {
-              cell[m * RP] = acc[n][c];
-              cell[m * RP + 8] = acc[n][2 + c];
-            }
-            acc[n][c] = acc[n][2 + c] = 0.0f;
-          }
-        }
-        cell += cell_floats;
+        for (int n = 0; n < NTM; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
         b = 0;
         ++tile;
         begin = true;
       }
     }
     __syncthreads();
-    const int cols = min(p.T, MOE_ENTRY);
     const float inv_line = __frcp_rn((float)line);
-    for (int o = tid; o < n_tiles * cols * 8; o += MOE_EXPERT_THREADS) {
-      const int f = o % 8, mt = o / 8, ti = mt / cols, m = mt - ti * cols;
-      const int64_t at = t0 + p0 + ti;
-      const int a = (int)(at / per_expert), s0 = l.start[a];
+    constexpr int COLS = 8 * NTM;  // 8 rows f x COLS tokens a tile
+    const int f = tid % 8, m = tid / 8 % COLS;
+    for (int ti = tid / (8 * COLS); ti < n_tiles; ti += MOE_EXPERT_THREADS / (8 * COLS)) {
+      const int a = (int)(((uint32_t)t0 + p0 + ti) / (uint32_t)per_expert), s0 = l.start[a];
       if (m >= l.start[a + 1] - s0) continue;
-      const float* q = cells + m * RP + f;
-      float gate = 0.0f, up = 0.0f;
       const int from = w4_first_cell<MOE_WARPS>(runs, ti, n_tiles, line, inv_line, nb);
       const int to = w4_first_cell<MOE_WARPS>(runs, ti + 1, n_tiles, line, inv_line, nb);
-      for (int c = from; c < to; ++c) {
-        gate = __fadd_rn(gate, q[c * cell_floats]);
-        up = __fadd_rn(up, q[c * cell_floats + 8]);
+      const float* q = cells + from * CELL + f * COLS + m;
+      float gate = 0.0f, up = 0.0f;
+      for (int c = from; c < to; ++c, q += CELL) {
+        gate = __fadd_rn(gate, q[0]);
+        up = __fadd_rn(up, q[8 * COLS]);
       }
       // silu(v) = v / (1 + exp(-v)); exp overflows to inf for very negative v, and v / inf is -0
       const float h = __fmul_rn(__fdiv_rn(gate, __fadd_rn(1.0f, expf(-gate))), up);
       uint32_t part[SH];
       split_bf16_stored<SH>(h, part);
-      const int64_t ff = (at - (int64_t)a * per_expert) * 8 + f;
+      const int64_t ff = (t0 + p0 + ti - (int64_t)a * per_expert) * 8 + f;
 #pragma unroll
       for (int s = 0; s < SH; ++s) p.h[((int64_t)s * p.T * p.top_k + s0 + m) * p.F + ff] = (uint16_t)part[s];
     }
@@ -495,9 +502,9 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_up_kernel(const Moe
 // Down: a tile is 16 rows d; its blocks are those of every entry in turn (a rank of a cluster takes
 // a share of that line, where there are few tiles).  A cell holds sums for every token, to which an
 // entry's are added with the tokens' weights when the warp leaves the entry.
-template <int NTM, int SH, int GW, bool ASYM>
+template <bool STAGED, int NTM, int SH, int GW, bool ASYM>
 __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_down_kernel(const MoeParams p) {
-  constexpr int SLOT = W4Slot<GW, ASYM>::BYTES, RP = W4_RP;
+  constexpr int SLOT = W4Slot<GW, ASYM>::BYTES, RP = MOE_RP;
   extern __shared__ __align__(16) char smem[];
   __shared__ W4Runs<MOE_WARPS> runs;
   const int tid = threadIdx.x, lane = tid % 32, g = lane / 4, t = lane % 4;
@@ -519,7 +526,16 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_down_kernel(const M
   __syncthreads();
   const int all = *l.active * nb, first = (int)((int64_t)all * rank / p.C);
   const int per_tile = (int)((int64_t)all * (rank + 1) / p.C) - first;
-  const int64_t plane = (int64_t)p.T * p.top_k * p.F * 2;
+  const int64_t hplane = (int64_t)slots * p.F * 2;
+  const int spitch = moe_row_pitch(p.F);
+  char* hs = smem + p.down_h_at;  // rows of every slot, part after part
+  if (STAGED) {
+    const int used = l.start[*l.active];
+    for (int s = 0; s < SH; ++s)
+      for (int m = 0; m < used; ++m)
+        moe_stage_row(hs + (s * slots + m) * spitch, reinterpret_cast<const char*>(p.h) + s * hplane + (int64_t)m * p.F * 2, p.F);
+  }
+  cp_commit();
 
   for (int p0 = 0; p0 < my_tiles; p0 += p.down_pass) {
     const int n_tiles = min(p.down_pass, my_tiles - p0), line = n_tiles * per_tile;
@@ -568,8 +584,11 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_down_kernel(const M
 #pragma unroll 1
       for (int u = 0; u < MOE_DEPTH - 1; ++u) issue(ring + u * SLOT);
 
+      cp_wait<MOE_DEPTH - 1>();  // h; the ring's units are younger
+      __syncthreads();
+
       float acc[NTM][4] = {};
-      const char* rows[NTM];
+      typename MoeRow<STAGED>::type rows[NTM];
       int s0 = 0, count = 0;
       bool begin = true, fresh = true;
       uint32_t slot = ring, spent = ring + (MOE_DEPTH - 1) * SLOT;
@@ -584,13 +603,17 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_down_kernel(const M
           count = l.start[a + 1] - s0;
 #pragma unroll
           for (int n = 0; n < NTM; ++n)
-            rows[n] = reinterpret_cast<const char*>(p.h + (int64_t)(s0 + min(8 * n + g, count - 1)) * p.F);
+            {
+              const int row = s0 + min(8 * n + g, count - 1);
+              rows[n] = MoeRow<STAGED>::of(smem_u32(hs) + row * spitch,
+                                           reinterpret_cast<const char*>(p.h) + (int64_t)row * p.F * 2, lane);
+            }
           begin = false;
         }
         cp_wait<MOE_DEPTH - 2>();
         __syncwarp();
         issue(spent);
-        moe_mac<SH, GW, ASYM>(acc, slot, lane, count, rows, plane, b, p.F);
+        moe_mac<STAGED, SH, GW, ASYM>(acc, slot, lane, count, rows, STAGED ? (int64_t)slots * spitch : hplane, b, p.F);
         spent = slot;
         slot = slot == ring + (MOE_DEPTH - 1) * SLOT ? ring : slot + SLOT;
         ++at;
@@ -681,40 +704,52 @@ int64_t up16(int64_t v) { return (v + 15) & ~(int64_t)15; }
 
 constexpr int64_t kSmemBudget = 226 * 1024;  // of 227 KB; the rest covers the static arrays
 
+// Tiles of a pass whose cells fit in `room`.
+int64_t moe_pass(int64_t room, int64_t cell, int64_t tiles) {
+  return std::min(tiles, room / cell - (sqk::MOE_WARPS - 1));
+}
+
 template <int NTM, int S, int SH, int GW, bool ASYM>
 cudaError_t launch_experts_t(sqk::MoeParams p, cudaStream_t st) {
-  const void* up = (const void*)sqk::moe_up_kernel<NTM, S, SH, GW, ASYM>;
-  const void* down = (const void*)sqk::moe_down_kernel<NTM, SH, GW, ASYM>;
-  for (const void* k : {up, down}) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBudget);
-    if (e != cudaSuccess) return e;
-  }
   const int64_t ring = (int64_t)sqk::MOE_WARPS * sqk::MOE_DEPTH * sqk::W4Slot<GW, ASYM>::BYTES;
+  const int64_t slots = (int64_t)p.T * p.top_k, lists = up16(sqk::MoeLists::ints(p.entries, slots) * 4);
+  const int64_t rings = std::max(ring, up16(sqk::MoeScratch::bytes(p.E, slots)));  // the lists' scratch comes before
   const int64_t sms = num_sms();
+  auto prepare = [](const void* k) {
+    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBudget);
+  };
   // gate and up: as many tiles a pass as a CTA can have, as far as their cells fit beside x, and x in
   // shared memory if half the tiles (at least eight) still have cells
   const int64_t per = ((int64_t)std::min(p.E, p.T * p.top_k) * (p.F / 8) + sms - 1) / sms;
-  const int64_t cell = (int64_t)std::min(p.T, sqk::MOE_ENTRY) * sqk::W4_RP * 4;
-  const int64_t x = (int64_t)S * p.T * (sqk::w4_blocks(p.D) * 256 + 64);
-  auto passes = [&](int64_t room, int64_t c, int64_t n) { return std::min(n, room / c - (sqk::MOE_WARPS - 1)); };
-  const int64_t slots = (int64_t)p.T * p.top_k, lists = up16(sqk::MoeLists::ints(p.entries, slots) * 4);
-  const int64_t rings = std::max(ring, sqk::MoeScratch::bytes(p.E, slots));  // the route's scratch comes before
-  p.x_staged = passes(kSmemBudget - lists - rings - x, cell, per) >= std::min<int64_t>(per, std::max<int64_t>(8, per / 2));
+  const int64_t cell = (int64_t)sqk::w4_cell_floats(NTM) * 4, x = (int64_t)S * p.T * sqk::moe_row_pitch(p.D);
+  const bool x_staged =
+      moe_pass(kSmemBudget - lists - rings - x, cell, per) >= std::min<int64_t>(per, std::max<int64_t>(8, per / 2));
   p.up_x_at = (int)lists;
-  p.up_cells_at = (int)(lists + (p.x_staged ? x : 0));
-  p.up_pass = (int)passes(kSmemBudget - rings - p.up_cells_at, cell, per);
+  p.up_cells_at = (int)(lists + (x_staged ? x : 0));
+  p.up_pass = (int)moe_pass(kSmemBudget - rings - p.up_cells_at, cell, per);
   p.up_ring_at = (int)(p.up_cells_at + (p.up_pass + sqk::MOE_WARPS - 1) * cell);
   cudaError_t e = cudaSuccess;
-  if (S > 1 && !p.x_staged) {
+  if (S > 1 && !x_staged) {
     e = launch_dependent((const void*)sqk::moe_split_kernel, (unsigned)sms, 1, 256, 0, 1, p, st);
     if (e != cudaSuccess) return e;
   }
+  const void* up = x_staged ? (const void*)sqk::moe_up_kernel<true, NTM, S, SH, GW, ASYM>
+                            : (const void*)sqk::moe_up_kernel<false, NTM, S, SH, GW, ASYM>;
+  e = prepare(up);
+  if (e != cudaSuccess) return e;
   e = launch_dependent(up, (unsigned)sms, 1, sqk::MOE_EXPERT_THREADS, (size_t)(p.up_ring_at + rings), 1, p, st);
   if (e != cudaSuccess) return e;
 
-  const int64_t tiles = (p.D + 15) / 16, cell2 = (int64_t)p.T * sqk::W4_RP * 4;
+  // down: 16-row tiles; clusters cut an entry line where there are few of them
+  const int64_t tiles = (p.D + 15) / 16, cell2 = (int64_t)p.T * sqk::MOE_RP * 4;
   p.C = 1;
   while (p.C < 8 && tiles * p.C * 2 <= sms) p.C *= 2;
+  const int64_t h = (int64_t)SH * slots * sqk::moe_row_pitch(p.F);
+  const bool h_staged = moe_pass(kSmemBudget - lists - ring - h, cell2, 2) >= 2;
+  const void* down = h_staged ? (const void*)sqk::moe_down_kernel<true, NTM, SH, GW, ASYM>
+                              : (const void*)sqk::moe_down_kernel<false, NTM, SH, GW, ASYM>;
+  e = prepare(down);
+  if (e != cudaSuccess) return e;
   int64_t clusters = std::min<int64_t>(tiles, sms / p.C);
   if (p.C > 1) {
     cudaLaunchConfig_t cfg{};
@@ -733,12 +768,14 @@ cudaError_t launch_experts_t(sqk::MoeParams p, cudaStream_t st) {
     clusters = std::min<int64_t>(clusters, std::max(active, 1));
   }
   const int64_t per2 = (tiles + clusters - 1) / clusters;
+  p.down_h_at = (int)lists;
+  p.down_cells_at = (int)(lists + (h_staged ? h : 0));
   // the sums over the ranks take the rings' place
-  p.down_pass = (int)std::min(passes(kSmemBudget - lists - ring, cell2, per2), std::max<int64_t>(1, ring / ((int64_t)p.T * 64)));
-  p.down_cells_at = (int)lists;
-  p.down_ring_at = (int)(lists + (p.down_pass + sqk::MOE_WARPS - 1) * cell2);
-  return launch_dependent(down, (unsigned)(clusters * p.C), 1, sqk::MOE_EXPERT_THREADS, (size_t)(p.down_ring_at + ring), p.C, p,
-                          st);
+  p.down_pass = (int)std::min(moe_pass(kSmemBudget - p.down_cells_at - ring, cell2, per2),
+                              std::max<int64_t>(1, ring / ((int64_t)p.T * 64)));
+  p.down_ring_at = (int)(p.down_cells_at + (p.down_pass + sqk::MOE_WARPS - 1) * cell2);
+  return launch_dependent(down, (unsigned)(clusters * p.C), 1, sqk::MOE_EXPERT_THREADS, (size_t)(p.down_ring_at + ring),
+                          p.C, p, st);
 }
 
 template <int S, int SH, int GW, bool ASYM>
@@ -774,12 +811,14 @@ static size_t moe_layout(sqk::MoeParams* p, char* base, int64_t T, int64_t D, in
   sqk::MoeParams q{};
   // every expert's last entry may be short
   q.entries = (int)std::min(T * k, E + T * k / sqk::MOE_ENTRY);
+  q.arrived = (unsigned int*)take(8 * sizeof(unsigned int));
   q.logits = (double*)take((size_t)(T * E) * 8);
   q.lists = (int*)take((size_t)sqk::MoeLists::ints(q.entries, T * k) * 4);
   q.xparts = (uint16_t*)take((size_t)(3 * T * D) * 2);
   q.h = (uint16_t*)take((size_t)(3 * T * k * F) * 2);
   if (p) {
     p->entries = q.entries;
+    p->arrived = q.arrived;
     p->logits = q.logits;
     p->lists = q.lists;
     p->xparts = q.xparts;
@@ -813,8 +852,8 @@ cudaError_t launch_moe_w4(const void* x, bool bf16, int64_t T, int64_t D, int64_
   p.renorm = renorm;
   p.ids = ids;
   p.wts = wts;
-  p.ids_in = ids_in;
-  p.wts_in = wts_in;
+  p.ids_in = wr ? ids : ids_in;
+  p.wts_in = wr ? wts : wts_in;
   p.w13 = (const char*)w13;
   p.s13 = s13;
   p.z13 = z13;

@@ -42,11 +42,28 @@ __device__ __forceinline__ void w4_unpack(uint32_t (&a)[4], uint32_t word, uint3
 // and a1, a3 of row g + 8 for the k pairs (2t, 2t + 1) and (2t + 8, 2t + 9), b0 and b1 of column g
 // for the same k, d0, d1 of row g, columns 2t, 2t + 1, and d2, d3 of row g + 8.  Which k the
 // sixteen slots stand for is free as long as A and B agree.
+// FIRST: D = A B.
+template <bool FIRST>
 __device__ __forceinline__ void w4_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if (FIRST)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// acc += scale * v for rows g (slo) and g + 8 (shi), two columns each.
+__device__ __forceinline__ void w4_scale_add(float (&acc)[4], float slo, float shi, const float (&v)[4]) {
+  const float2 a = __ffma2_rn(make_float2(slo, slo), make_float2(v[0], v[1]), make_float2(acc[0], acc[1]));
+  const float2 b = __ffma2_rn(make_float2(shi, shi), make_float2(v[2], v[3]), make_float2(acc[2], acc[3]));
+  acc[0] = a.x;
+  acc[1] = a.y;
+  acc[2] = b.x;
+  acc[3] = b.y;
 }
 
 // x as a sum of bf16 numbers.  Parts are cut off, not rounded, so a finite x is exactly the sum of
@@ -91,8 +108,10 @@ __device__ __forceinline__ void split_bf16_stored(float x, uint32_t part[S]) {
 // (and a __syncwarp for the scales, which also says that the last unit's slot has been read and can
 // be filled again).  Registers hold one block, whatever the depth.
 //   What sets the depth is latency: at 6.5 TB/s and about 1 us under load an SM needs some 45 KB in
-// flight; 16 warps with two units each on their way have 64 KB.  What limits the loop once the bytes
-// are there is the unpacking (56 shifts and logic operations a block on the half-rate integer pipe,
+// flight; 16 warps with a unit each on its way and one at work have 32 to 64 KB, and asking the L2 for
+// 256 bytes where the copies take 128 of a row fetches what the warp wants next (231 MB of weights: 47.8
+// us with the hint, 55.7 without; DEPTH 3 is 3 % faster there and 10 % slower at 30 MB).  What limits the
+// loop once the bytes are there is the unpacking (56 shifts and logic operations a block on the half-rate integer pipe,
 // about 29 clocks of an SM, against 46 in which HBM delivers a block), so everything else in it is
 // kept few: two blocks to a unit halve the control and address arithmetic.
 constexpr int W4_UNIT = 2 * W4_BLOCK;
@@ -116,7 +135,7 @@ struct W4Slot {  // of the ring: per block, codes of rows g and of rows g + 8; t
 
 // 16 bytes, or zeros where `bytes` is 0.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes = 16) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async16_if(bool on, uint32_t dst, const void* src) {
   asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(dst),
@@ -236,8 +255,6 @@ __device__ __forceinline__ void w4_mac(float (&acc)[NTA][4], uint32_t slot, int 
           zlo = w4_zero(lds8(slot + L::ZEROS + q * 16 + row));
           zhi = w4_zero(lds8(slot + L::ZEROS + q * 16 + 8 + row));
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) tmp[n][0] = tmp[n][1] = tmp[n][2] = tmp[n][3] = 0.0f;
       }
       uint32_t a[4], c[4];
       w4_unpack(a, lo[i], zlo);
@@ -247,20 +264,16 @@ __device__ __forceinline__ void w4_mac(float (&acc)[NTA][4], uint32_t slot, int 
 #pragma unroll
         for (int s = 0; s < S; ++s) {
           const uint4 x = xload(n, s, 4 * b + i);
-          w4_mma(tmp[n], a[0], c[0], a[1], c[1], x.x, x.y);
-          w4_mma(tmp[n], a[2], c[2], a[3], c[3], x.z, x.w);
+          if (i % GW == 0 && s == 0) w4_mma<true>(tmp[n], a[0], c[0], a[1], c[1], x.x, x.y);
+          else w4_mma<false>(tmp[n], a[0], c[0], a[1], c[1], x.x, x.y);
+          w4_mma<false>(tmp[n], a[2], c[2], a[3], c[3], x.z, x.w);
         }
       }
       if (i % GW == GW - 1) {
         const float slo = bf16lo(lds16(slot + L::SCALES + q * 32 + row * 2));
         const float shi = bf16lo(lds16(slot + L::SCALES + q * 32 + 16 + row * 2));
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          acc[n][0] = __fmaf_rn(slo, tmp[n][0], acc[n][0]);
-          acc[n][1] = __fmaf_rn(slo, tmp[n][1], acc[n][1]);
-          acc[n][2] = __fmaf_rn(shi, tmp[n][2], acc[n][2]);
-          acc[n][3] = __fmaf_rn(shi, tmp[n][3], acc[n][3]);
-        }
+        for (int n = 0; n < NT; ++n) w4_scale_add(acc[n], slo, shi, tmp[n]);
       }
     }
   }
@@ -270,7 +283,19 @@ __device__ __forceinline__ void w4_mac(float (&acc)[NTA][4], uint32_t slot, int 
 // A CTA's line of units (tile after tile) is cut into equal runs, one a warp.  A warp's sum over its
 // part of a tile goes to a cell of its own; the cells of a tile are then added in the order of the
 // warps.  Cells lie in the order of the line, so there is at most one more per run than tiles.
-constexpr int W4_RP = 20;  // floats between a cell's tokens: 16 rows, padded to spread the banks
+//   A cell of NT column tiles is 16 rows x 8 NT columns; a lane's pairs of columns leave in one store
+// each, and half a warp's cover the banks once.
+__host__ __device__ constexpr int w4_cell_floats(int NT) { return 128 * NT; }
+
+template <int NT, int NTA>
+__device__ __forceinline__ void w4_put_cell(float* cell, const float (&acc)[NTA][4], int lane) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    float* q = cell + (lane / 4) * (8 * NTA) + 8 * n + 2 * (lane % 4);
+    *reinterpret_cast<float2*>(q) = make_float2(acc[n][0], acc[n][1]);
+    *reinterpret_cast<float2*>(q + 8 * (8 * NTA)) = make_float2(acc[n][2], acc[n][3]);
+  }
+}
 
 template <int WARPS>
 struct W4Runs {  // in shared memory

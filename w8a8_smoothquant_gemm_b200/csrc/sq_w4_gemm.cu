@@ -23,7 +23,7 @@
 namespace sqk {
 
 constexpr int W4G_WARPS = 16;  // of a CTA
-constexpr int W4G_DEPTH = 3;   // slots of a warp's ring
+constexpr int W4G_DEPTH = 2;   // slots of a warp's ring
 
 struct W4GemmParams {
   const char* x;
@@ -48,7 +48,7 @@ struct W4GemmParams {
 
 template <int NT, int S, int GW, bool ASYM, bool ALIGNED>
 __global__ void __launch_bounds__(32 * W4G_WARPS, 1) w4_gemm_kernel(const W4GemmParams p) {
-  constexpr int WARPS = W4G_WARPS, THREADS = 32 * WARPS, DEPTH = W4G_DEPTH, SLOT = W4Slot<GW, ASYM>::BYTES, RP = W4_RP;
+  constexpr int WARPS = W4G_WARPS, THREADS = 32 * WARPS, DEPTH = W4G_DEPTH, SLOT = W4Slot<GW, ASYM>::BYTES, CELL = w4_cell_floats(NT);
   extern __shared__ __align__(16) char smem[];
   __shared__ W4Runs<WARPS> runs;
   const int tid = threadIdx.x, lane = tid % 32, g = lane / 4, t = lane % 4;
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(32 * W4G_WARPS, 1) w4_gemm_kernel(const W4Gemm
   const int my_tiles = p.tile_q + (cluster < p.tile_r);
   const uint32_t last_row = (uint32_t)min(p.N - 1 - t0 * 16, (int64_t)my_tiles * 16 - 1);
   float* out = reinterpret_cast<float*>(smem + p.out_at);     // [tile of the pass][token][row]
-  float* cells = reinterpret_cast<float*>(smem + p.cell_at);  // [cell][token][row], padded
+  float* cells = reinterpret_cast<float*>(smem + p.cell_at);  // [cell][row][8 NT]
   const uint32_t ring = smem_u32(smem + p.ring_at) + warp * DEPTH * SLOT;
   W4Base base = p.w;
   base.codes += t0 * 16 * base.row_bytes;
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(32 * W4G_WARPS, 1) w4_gemm_kernel(const W4Gemm
       {
         const W4Run run = w4_runs<WARPS>(runs, line, units, warp, lane);
         int b = run.b, left = run.units;
-        float* cell = cells + run.cell * Mr * RP + g;
+        float* cell = cells + run.cell * CELL;
 
         int to_load = left, load_tile = run.tile, load_b = units - b;
         W4Cursor cur = w4_place<GW, ASYM, ALIGNED>(base, (p0 + load_tile) * 16, (p0 + load_tile) * 16 + 8, last_row, c0 + b, lane);
@@ -160,19 +160,10 @@ __global__ void __launch_bounds__(32 * W4G_WARPS, 1) w4_gemm_kernel(const W4Gemm
             xo += 2 * W4_UNIT;
           }
           {  // the end of this warp's part of the tile
+            w4_put_cell<NT>(cell, acc, lane);
+            cell += CELL;
 #pragma unroll
-            for (int k = 0; k < NT; ++k) {
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const int m = 8 * k + 2 * t + c;
-                if (m < Mr) {
-                  cell[m * RP] = acc[k][c];
-                  cell[m * RP + 8] = acc[k][2 + c];
-                }
-                acc[k][c] = acc[k][2 + c] = 0.0f;
-              }
-            }
-            cell += Mr * RP;
+            for (int k = 0; k < NT; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.0f;
             b = 0;
             xo = 0;
           }
@@ -187,10 +178,10 @@ __global__ void __launch_bounds__(32 * W4G_WARPS, 1) w4_gemm_kernel(const W4Gemm
         const int from = w4_first_cell<WARPS>(runs, ti, n_tiles, line, inv_line, units);
         const int to = w4_first_cell<WARPS>(runs, ti + 1, n_tiles, line, inv_line, units);
         if (m >= Mr) continue;
-        const float* q = cells + (from * Mr + m) * RP + row;
+        const float* q = cells + from * CELL + row * (8 * NT) + m;
         const int o = (ti * Mr + m) * 16 + row;
         float v = c0 == b0 ? 0.0f : out[o];
-        for (int c = from; c < to; ++c, q += Mr * RP) v = __fadd_rn(v, *q);
+        for (int c = from; c < to; ++c, q += CELL) v = __fadd_rn(v, *q);
         const int64_t n = (t0 + p0 + ti) * 16 + row;
         if (p.C > 1 || !last) out[o] = v;
         else if (n < p.N) store_out(p.y, (m0 + m) * p.ldy + n, v, p.y_bf16);
@@ -219,17 +210,6 @@ namespace {
 
 constexpr int64_t kSmemBudget = 226 * 1024;  // of 227 KB; the rest covers the static arrays
 
-// Cells of a pass of n tiles of `units` units: one for each tile that a warp's run touches.
-int64_t w4_cells(int64_t n, int64_t units, int warps) {
-  const int64_t line = n * units;
-  int64_t c = 0;
-  for (int w = 0; w < warps; ++w) {
-    const int64_t a0 = line * w / warps, a1 = line * (w + 1) / warps;
-    if (a1 > a0) c += (a1 - 1) / units - a0 / units + 1;
-  }
-  return c;
-}
-
 // Launches if x and the sums fit in shared memory whole, or if `chunks` allows pieces; *fits says.
 template <int NT, int S, int GW, bool ASYM, bool ALIGNED>
 cudaError_t launch_w4_gemm_t(sqk::W4GemmParams p, bool chunks, bool* fits, cudaStream_t st) {
@@ -248,7 +228,7 @@ cudaError_t launch_w4_gemm_t(sqk::W4GemmParams p, bool chunks, bool* fits, cudaS
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   const int64_t ring = (int64_t)WARPS * sqk::W4G_DEPTH * sqk::W4Slot<GW, ASYM>::BYTES;
-  const int64_t cell = (int64_t)mr * sqk::W4_RP * 4, out = (int64_t)mr * 16 * 4;  // bytes per cell, per tile
+  const int64_t cell = (int64_t)sqk::w4_cell_floats(NT) * 4, out = (int64_t)mr * 16 * 4;  // bytes per cell, per tile
   const int64_t x_unit = (int64_t)S * mr * (2 * sqk::W4_UNIT), x_fixed = (int64_t)S * mr * 64;
   // The cluster: as few CTAs as hold x and the sums of their tiles whole, or, with few tiles, as many
   // as still give every CTA an SM; each keeps at least two units of a tile.
@@ -271,18 +251,21 @@ cudaError_t launch_w4_gemm_t(sqk::W4GemmParams p, bool chunks, bool* fits, cudaS
       p.clusters = (int)std::min<int64_t>(p.clusters, std::max<int64_t>(1, active / mt));
     }
     const int64_t per = (tiles + p.clusters - 1) / p.clusters;
-    int64_t n_cells = 0;  // CTAs have per or per - 1 tiles, ranks units or units - 1 units of each
-    for (int64_t n = std::max<int64_t>(1, per - 1); n <= per; ++n)
-      for (int64_t u = nu / C; u <= units; ++u) n_cells = std::max(n_cells, w4_cells(n, u, WARPS));
-    const int64_t sums = C > 1 ? per * out : 0;
-    p.chunk = (int)units;
-    p.pass = (int)per;
-    p.cell_at = (int)(x_fixed + units * x_unit);
-    p.ring_at = p.out_at = (int)(p.cell_at + n_cells * cell);
-    used = p.ring_at + std::max(ring, sums);
-    *fits = used <= kSmemBudget;
+    // tiles whose cells fit beside x, the whole of it: all of them, or passes of at least 16
+    const int64_t x_all = x_fixed + units * x_unit;
+    int64_t cap = (kSmemBudget - x_all - ring) / cell - (WARPS - 1);
+    if (C > 1) cap = std::min(cap, ring / out);  // their sums take the rings' place
+    *fits = cap >= std::min<int64_t>(per, 16);
     if (more && (!*fits || tiles * C * 2 <= sms)) continue;
-    if (*fits) break;
+    if (*fits) {
+      const int64_t passes = (per + cap - 1) / cap;
+      p.pass = (int)((per + passes - 1) / passes);
+      p.chunk = (int)units;
+      p.cell_at = (int)x_all;
+      p.ring_at = p.out_at = (int)(x_all + (p.pass + WARPS - 1) * cell);
+      used = p.ring_at + ring;
+      break;
+    }
     if (!chunks) return cudaSuccess;
     // x in chunks, tiles in passes: a pass of t tiles has at most t + WARPS - 1 cells
     const int64_t room = kSmemBudget - ring - x_fixed - (WARPS - 1) * cell;
