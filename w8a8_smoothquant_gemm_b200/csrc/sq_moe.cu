@@ -341,11 +341,16 @@ struct MoeRow<true> {
 // Bytes between staged rows of K bf16 numbers: whole units, rows 64 bytes apart modulo 128.
 __host__ __device__ __forceinline__ int moe_row_pitch(int K) { return w4_units(K) * (2 * W4_UNIT) + 64; }
 
-// Starts the copies of a row of K bf16 numbers to shared memory, with zeros up to whole units.
-__device__ __forceinline__ void moe_stage_row(char* dst, const char* src, int K) {
-  for (int v = threadIdx.x; v < w4_units(K) * (W4_UNIT / 8); v += MOE_EXPERT_THREADS) {
-    if (v * 8 < K) cp_async16(smem_u32(dst + v * 16), src + v * 16);
-    else *reinterpret_cast<uint4*>(dst + v * 16) = make_uint4(0, 0, 0, 0);
+// Starts the copies of `rows` rows of K bf16 numbers (row r at src(r)) to shared memory, with zeros up to
+// whole units.
+template <typename Src>
+__device__ __forceinline__ void moe_stage_rows(char* dst, int rows, int K, Src src) {
+  const int pieces = w4_units(K) * (W4_UNIT / 8), pitch = moe_row_pitch(K);
+  const float inv = __frcp_rn((float)pieces);
+  for (int i = threadIdx.x; i < rows * pieces; i += MOE_EXPERT_THREADS) {
+    const int r = w4_div(i, pieces, inv), v = i - r * pieces;
+    if (v * 8 < K) cp_async16(smem_u32(dst + r * pitch + v * 16), src(r) + v * 16);
+    else *reinterpret_cast<uint4*>(dst + r * pitch + v * 16) = make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -369,8 +374,7 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_up_kernel(const Moe
   const MoeLists l(reinterpret_cast<int*>(smem), p.entries, slots);
   wait_for_previous_kernel();
   allow_dependent_launch();
-  if (STAGED && S == 1)
-    for (int m = 0; m < p.T; ++m) moe_stage_row(xs + m * spitch, p.x + m * p.ldx_bytes, p.D);
+  if (STAGED && S == 1) moe_stage_rows(xs, p.T, p.D, [&](int r) { return p.x + r * p.ldx_bytes; });
   cp_commit();
   moe_route(p, l, smem + p.up_ring_at, warp_sums);
   if (blockIdx.x == 0)  // for the down kernel
@@ -421,20 +425,21 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_up_kernel(const Moe
 #pragma unroll 1
     for (int u = 0; u < MOE_DEPTH - 1; ++u) issue(ring + u * SLOT);
     if (STAGED && S > 1 && p0 == 0) {
-      for (int m = 0; m < p.T; ++m) {
+      const int pieces = nb * (W4_UNIT / 8);
+      const float inv = __frcp_rn((float)pieces);
+      for (int i = tid; i < p.T * pieces; i += MOE_EXPERT_THREADS) {
+        const int m = w4_div(i, pieces, inv), v = i - m * pieces;
         const float* src = reinterpret_cast<const float*>(p.x + m * p.ldx_bytes);
-        for (int v = tid; v < nb * (W4_UNIT / 8); v += MOE_EXPERT_THREADS) {
-          float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-          if (v * 8 < p.D) load8<false>(reinterpret_cast<const char*>(src + v * 8), f);
-          uint32_t part[8][S];
+        float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (v * 8 < p.D) load8<false>(reinterpret_cast<const char*>(src + v * 8), f);
+        uint32_t part[8][S];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) split_bf16<S>(f[e], part[e]);
+        for (int e = 0; e < 8; ++e) split_bf16<S>(f[e], part[e]);
 #pragma unroll
-          for (int s = 0; s < S; ++s)
-            *reinterpret_cast<uint4*>(xs + (s * p.T + m) * spitch + v * 16) =
-                make_uint4(part[0][s] | (part[1][s] << 16), part[2][s] | (part[3][s] << 16),
-                           part[4][s] | (part[5][s] << 16), part[6][s] | (part[7][s] << 16));
-        }
+        for (int s = 0; s < S; ++s)
+          *reinterpret_cast<uint4*>(xs + (s * p.T + m) * spitch + v * 16) =
+              make_uint4(part[0][s] | (part[1][s] << 16), part[2][s] | (part[3][s] << 16),
+                         part[4][s] | (part[5][s] << 16), part[6][s] | (part[7][s] << 16));
       }
     }
     cp_wait<MOE_DEPTH - 1>();  // x; the ring's units are younger
@@ -532,8 +537,8 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_down_kernel(const M
   if (STAGED) {
     const int used = l.start[*l.active];
     for (int s = 0; s < SH; ++s)
-      for (int m = 0; m < used; ++m)
-        moe_stage_row(hs + (s * slots + m) * spitch, reinterpret_cast<const char*>(p.h) + s * hplane + (int64_t)m * p.F * 2, p.F);
+      moe_stage_rows(hs + s * slots * spitch, used, p.F,
+                     [&](int r) { return reinterpret_cast<const char*>(p.h) + s * hplane + (int64_t)r * p.F * 2; });
   }
   cp_commit();
 

@@ -84,13 +84,13 @@ __global__ void __launch_bounds__(32 * W4G_WARPS, 1) w4_gemm_kernel(const W4Gemm
       if (c0 != b0 || p0 != 0) __syncthreads();  // x, the cells and the sums of the last turn have been read
       const bool stage = !whole || p0 == 0;
       const int vecs = units * (W4_UNIT / 8);  // 8-value pieces per token
+      const float inv_vecs = __frcp_rn((float)vecs);
       if (S == 1 && stage) {
-        for (int m = 0; m < Mr; ++m) {
-          const char* src = p.x + (m0 + m) * p.ldx_bytes + (int64_t)c0 * W4_UNIT * 2;
-          for (int v = tid; v < vecs; v += THREADS) {
-            if (c0 * W4_UNIT + v * 8 < p.K) cp_async16(smem_u32(smem + m * pitch + v * 16), src + v * 16);
-            else *reinterpret_cast<uint4*>(smem + m * pitch + v * 16) = make_uint4(0, 0, 0, 0);
-          }
+        const char* src = p.x + m0 * p.ldx_bytes + (int64_t)c0 * W4_UNIT * 2;
+        for (int i = tid; i < Mr * vecs; i += THREADS) {
+          const int m = w4_div(i, vecs, inv_vecs), v = i - m * vecs;
+          if (c0 * W4_UNIT + v * 8 < p.K) cp_async16(smem_u32(smem + m * pitch + v * 16), src + m * p.ldx_bytes + v * 16);
+          else *reinterpret_cast<uint4*>(smem + m * pitch + v * 16) = make_uint4(0, 0, 0, 0);
         }
       }
       cp_commit();
@@ -118,23 +118,23 @@ __global__ void __launch_bounds__(32 * W4G_WARPS, 1) w4_gemm_kernel(const W4Gemm
 #pragma unroll 1
         for (int u = 0; u < DEPTH - 1; ++u) issue(ring + u * SLOT);
         if (S > 1 && stage) {
-          for (int m = 0; m < Mr; ++m) {
-            const char* src = p.x + (m0 + m) * p.ldx_bytes + (int64_t)c0 * W4_UNIT * 4;
-            for (int v2 = tid; v2 < vecs; v2 += THREADS) {
-              float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-              if (c0 * W4_UNIT + v2 * 8 < p.K) {
-                *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(src + v2 * 32);
-                *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(src + v2 * 32 + 16);
-              }
-              uint32_t part[8][S];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) split_bf16<S>(f[e], part[e]);
-#pragma unroll
-              for (int s = 0; s < S; ++s)
-                *reinterpret_cast<uint4*>(smem + m * pitch + v2 * 16 + s * plane) =
-                    make_uint4(part[0][s] | (part[1][s] << 16), part[2][s] | (part[3][s] << 16),
-                               part[4][s] | (part[5][s] << 16), part[6][s] | (part[7][s] << 16));
+          const char* src = p.x + m0 * p.ldx_bytes + (int64_t)c0 * W4_UNIT * 4;
+          for (int i = tid; i < Mr * vecs; i += THREADS) {
+            const int m = w4_div(i, vecs, inv_vecs), v = i - m * vecs;
+            float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (c0 * W4_UNIT + v * 8 < p.K) {
+              const float4* at = reinterpret_cast<const float4*>(src + m * p.ldx_bytes + v * 32);
+              *reinterpret_cast<float4*>(f) = at[0];
+              *reinterpret_cast<float4*>(f + 4) = at[1];
             }
+            uint32_t part[8][S];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) split_bf16<S>(f[e], part[e]);
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+              *reinterpret_cast<uint4*>(smem + m * pitch + v * 16 + s * plane) =
+                  make_uint4(part[0][s] | (part[1][s] << 16), part[2][s] | (part[3][s] << 16),
+                             part[4][s] | (part[5][s] << 16), part[6][s] | (part[7][s] << 16));
           }
         }
         cp_wait<DEPTH - 1>();  // x; the ring's blocks are younger
@@ -210,9 +210,8 @@ namespace {
 
 constexpr int64_t kSmemBudget = 226 * 1024;  // of 227 KB; the rest covers the static arrays
 
-// Launches if x and the sums fit in shared memory whole, or if `chunks` allows pieces; *fits says.
 template <int NT, int S, int GW, bool ASYM, bool ALIGNED>
-cudaError_t launch_w4_gemm_t(sqk::W4GemmParams p, bool chunks, bool* fits, cudaStream_t st) {
+cudaError_t launch_w4_gemm_t(sqk::W4GemmParams p, cudaStream_t st) {
   constexpr int WARPS = sqk::W4G_WARPS;
   auto kern = sqk::w4_gemm_kernel<NT, S, GW, ASYM, ALIGNED>;
   const int64_t tiles = (p.N + 15) / 16, mt = (p.M + 8 * NT - 1) / (8 * NT);
@@ -255,9 +254,9 @@ cudaError_t launch_w4_gemm_t(sqk::W4GemmParams p, bool chunks, bool* fits, cudaS
     const int64_t x_all = x_fixed + units * x_unit;
     int64_t cap = (kSmemBudget - x_all - ring) / cell - (WARPS - 1);
     if (C > 1) cap = std::min(cap, ring / out);  // their sums take the rings' place
-    *fits = cap >= std::min<int64_t>(per, 16);
-    if (more && (!*fits || tiles * C * 2 <= sms)) continue;
-    if (*fits) {
+    const bool fits = cap >= std::min<int64_t>(per, 16);
+    if (more && (!fits || tiles * C * 2 <= sms)) continue;
+    if (fits) {
       const int64_t passes = (per + cap - 1) / cap;
       p.pass = (int)((per + passes - 1) / passes);
       p.chunk = (int)units;
@@ -266,7 +265,6 @@ cudaError_t launch_w4_gemm_t(sqk::W4GemmParams p, bool chunks, bool* fits, cudaS
       used = p.ring_at + ring;
       break;
     }
-    if (!chunks) return cudaSuccess;
     // x in chunks, tiles in passes: a pass of t tiles has at most t + WARPS - 1 cells
     const int64_t room = kSmemBudget - ring - x_fixed - (WARPS - 1) * cell;
     p.pass = (int)std::max<int64_t>(1, std::min(per, (room / 2) / (out + cell)));
@@ -276,7 +274,6 @@ cudaError_t launch_w4_gemm_t(sqk::W4GemmParams p, bool chunks, bool* fits, cudaS
     p.cell_at = (int)(p.out_at + p.pass * out);
     p.ring_at = (int)(p.cell_at + (p.pass + WARPS - 1) * cell);
     used = p.ring_at + ring;
-    *fits = true;
     break;
   }
   p.tile_q = (int)(tiles / p.clusters);
@@ -293,22 +290,22 @@ cudaError_t launch_w4_gemm_t(sqk::W4GemmParams p, bool chunks, bool* fits, cudaS
 }
 
 template <int NT, int S, int GW, bool ASYM>
-cudaError_t launch_w4_gemm_a(const sqk::W4GemmParams& p, bool chunks, bool* fits, cudaStream_t st) {
+cudaError_t launch_w4_gemm_a(const sqk::W4GemmParams& p, cudaStream_t st) {
   const bool aligned = p.N % 8 == 0 && (uintptr_t)p.w.scales % 16 == 0 && (uintptr_t)p.w.zeros % 8 == 0;
-  return aligned ? launch_w4_gemm_t<NT, S, GW, ASYM, true>(p, chunks, fits, st)
-                 : launch_w4_gemm_t<NT, S, GW, ASYM, false>(p, chunks, fits, st);
+  return aligned ? launch_w4_gemm_t<NT, S, GW, ASYM, true>(p, st)
+                 : launch_w4_gemm_t<NT, S, GW, ASYM, false>(p, st);
 }
 
 template <int NT, int S>
-cudaError_t launch_w4_gemm_g(const sqk::W4GemmParams& p, int group, bool chunks, bool* fits, cudaStream_t st) {
+cudaError_t launch_w4_gemm_g(const sqk::W4GemmParams& p, int group, cudaStream_t st) {
   if (p.w.zeros) {
-    if (group == 32) return launch_w4_gemm_a<NT, S, 1, true>(p, chunks, fits, st);
-    if (group == 64) return launch_w4_gemm_a<NT, S, 2, true>(p, chunks, fits, st);
-    return launch_w4_gemm_a<NT, S, 4, true>(p, chunks, fits, st);
+    if (group == 32) return launch_w4_gemm_a<NT, S, 1, true>(p, st);
+    if (group == 64) return launch_w4_gemm_a<NT, S, 2, true>(p, st);
+    return launch_w4_gemm_a<NT, S, 4, true>(p, st);
   }
-  if (group == 32) return launch_w4_gemm_a<NT, S, 1, false>(p, chunks, fits, st);
-  if (group == 64) return launch_w4_gemm_a<NT, S, 2, false>(p, chunks, fits, st);
-  return launch_w4_gemm_a<NT, S, 4, false>(p, chunks, fits, st);
+  if (group == 32) return launch_w4_gemm_a<NT, S, 1, false>(p, st);
+  if (group == 64) return launch_w4_gemm_a<NT, S, 2, false>(p, st);
+  return launch_w4_gemm_a<NT, S, 4, false>(p, st);
 }
 
 }  // namespace
@@ -331,17 +328,11 @@ cudaError_t launch_w4_gemm(const void* x, bool bf16, int64_t M, int64_t K, int64
   p.y = y;
   p.ldy = ldy;
   p.y_bf16 = y_bf16;
-  bool fits = false;
-  if (bf16) {
-    if (M <= 8) return launch_w4_gemm_g<1, 1>(p, group, true, &fits, st);
-    if (M > 16) {
-      const cudaError_t e = launch_w4_gemm_g<4, 1>(p, group, false, &fits, st);
-      if (e != cudaSuccess || fits) return e;
-    }
-    return launch_w4_gemm_g<2, 1>(p, group, true, &fits, st);
-  }
-  if (M <= 8) return launch_w4_gemm_g<1, 3>(p, group, true, &fits, st);
-  return launch_w4_gemm_g<2, 3>(p, group, true, &fits, st);
+  // up to 8 tokens fill a column tile; more take blocks of 16 (grid y), each reading the weights again,
+  // from L2: a CTA that held 32 or more tokens would have room for too few tiles' sums beside x (64 tokens,
+  // 4096 x 4096: 16 us against 19 to 39)
+  if (bf16) return M <= 8 ? launch_w4_gemm_g<1, 1>(p, group, st) : launch_w4_gemm_g<2, 1>(p, group, st);
+  return M <= 8 ? launch_w4_gemm_g<1, 3>(p, group, st) : launch_w4_gemm_g<2, 3>(p, group, st);
 }
 
 }  // namespace sqh
