@@ -466,35 +466,45 @@ def sq_selfcheck_shared_divisor(a: torch.Tensor, b: torch.Tensor, want_quotients
 # ----------------------------------------------------------------------------- 4-bit weights
 # A packed weight is (wq [N, sq_w4_row_bytes(K)] uint8, sg [ceil(K / group), N] bfloat16, zp uint8
 # like sg or None); experts stack these on a leading dimension.  Calls run on the tensors' own
-# device: its current stream is taken unless `stream` is given.
+# device: its current stream is taken unless `stream` is given.  In decode a call's host time
+# counts, so what can be wrong is looked at in few steps and named in a second look.
 def sq_w4_row_bytes(K: int) -> int:
     return (K + 127) // 128 * 64
 
 
-def _on(dev: torch.device, stream):
-    """The stream to launch on, and the device switch it needs (None where it is current already)."""
-    if dev.type != "cuda":
-        raise ValueError("expected CUDA tensors")
-    cur = torch.cuda.current_device()
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError("the stream belongs to another device than the tensors")
-        raw = stream.cuda_stream
-    else:
-        raw = torch._C._cuda_getCurrentRawStream(dev.index)
-    return raw, None if dev.index == cur else torch.cuda.device(dev)
+_BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
+_FDT = {_BF16: SQ_BF16, _F32: SQ_F32}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(fn: str, dev: torch.device, stream, *args):
-    raw, switch = _on(dev, stream)
+    """One library call on `dev`, made the current device for it if it is not."""
+    if dev.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    if stream is None:
+        raw = _raw_stream(dev.index)
+    elif stream.device != dev:
+        raise ValueError("the stream belongs to another device than the tensors")
+    else:
+        raw = stream.cuda_stream
     f = getattr(_lib or lib(), fn)
-    if switch is None:
+    if dev.index == _current_device():
         status = f(*args, raw)
     else:
-        with switch:
+        with torch.cuda.device(dev):
             status = f(*args, raw)
     if status != 0:
         raise SQError(fn, status)
+
+
+def _float_mat(t: torch.Tensor, name: str) -> int:
+    """The library's type of a bfloat16 or float32 matrix with unit column stride."""
+    dt = _FDT.get(t.dtype)
+    if dt is None or not t.is_cuda or t.dim() != 2 or t.stride(1) != 1:
+        _mat(t, name)
+        _dt(t)
+    return dt
 
 
 def _packed(name: str, wq, sg, zp, lead: tuple, K: int, group: int, dev):
@@ -502,11 +512,11 @@ def _packed(name: str, wq, sg, zp, lead: tuple, K: int, group: int, dev):
     if group not in (32, 64, 128):
         raise ValueError("group must be 32, 64 or 128")
     gshape = (*lead[:-1], (K + group - 1) // group, lead[-1])
-    if wq.dtype != torch.uint8 or wq.shape != (*lead, sq_w4_row_bytes(K)) or not wq.is_contiguous() or wq.device != dev:
+    if wq.shape != (*lead, (K + 127) // 128 * 64) or wq.dtype is not _U8 or not wq.is_contiguous() or wq.device != dev:
         raise ValueError(f"{name}: codes must be contiguous uint8 {(*lead, sq_w4_row_bytes(K))} on the input's device")
-    if sg.dtype != torch.bfloat16 or sg.shape != gshape or not sg.is_contiguous() or sg.device != dev:
+    if sg.shape != gshape or sg.dtype is not _BF16 or not sg.is_contiguous() or sg.device != dev:
         raise ValueError(f"{name}: scales must be contiguous bfloat16 {gshape} on the input's device")
-    if zp is not None and (zp.dtype != torch.uint8 or zp.shape != gshape or not zp.is_contiguous() or zp.device != dev):
+    if zp is not None and (zp.shape != gshape or zp.dtype is not _U8 or not zp.is_contiguous() or zp.device != dev):
         raise ValueError(f"{name}: zero points must be contiguous uint8 {gshape} on the input's device")
 
 
@@ -514,18 +524,16 @@ def _ptr0(t):
     return None if t is None else t.data_ptr()
 
 
-def _out(y, shape: tuple, dtype, dev):
+def _out(like, y, shape: tuple, dtype):
+    """y, or a new tensor on the device of `like`; and the library's type of it."""
     if y is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    if y.shape != shape or y.device != dev or y.stride(-1) != 1:
+        y = like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
+    elif y.shape != shape or y.device != like.device or y.stride(-1) != 1:
         raise ValueError(f"y must be {shape} with unit column stride, on the input's device")
-    return y
-
-
-def _odt(t: torch.Tensor) -> int:
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"expected a bfloat16 or float32 output, got {t.dtype}")
-    return SQ_BF16 if t.dtype == torch.bfloat16 else SQ_F32
+    dt = _FDT.get(y.dtype)
+    if dt is None:
+        raise TypeError(f"expected a bfloat16 or float32 output, got {y.dtype}")
+    return y, dt
 
 
 def sq_fold_quant_weights_w4(W: torch.Tensor, s: torch.Tensor | None = None, gamma: torch.Tensor | None = None,
@@ -533,26 +541,29 @@ def sq_fold_quant_weights_w4(W: torch.Tensor, s: torch.Tensor | None = None, gam
                              wq: torch.Tensor | None = None, sg: torch.Tensor | None = None,
                              zp: torch.Tensor | None = None, stream=None):
     """W [K, N] -> (wq packed, sg, zp or None, gamma / s or None, beta / s or None).  asym: with zero points."""
-    W = _mat(W, "W")
+    dt = _float_mat(W, "W")
     K, N = W.shape
     dev = W.device
     for v, name in ((s, "s"), (gamma, "gamma"), (beta, "beta")):
-        _vec(v, K, name)
-        if v is not None and v.device != dev:
-            raise ValueError(f"{name} must be on W's device")
+        if v is not None:
+            _vec(v, K, name)
+            if v.device != dev:
+                raise ValueError(f"{name} must be on W's device")
     if group not in (32, 64, 128):
         raise ValueError("group must be 32, 64 or 128")
     groups = (K + group - 1) // group
-    wq = torch.empty(N, sq_w4_row_bytes(K), dtype=torch.uint8, device=dev) if wq is None else wq
-    sg = torch.empty(groups, N, dtype=torch.bfloat16, device=dev) if sg is None else sg
     if not asym and zp is not None:
         raise ValueError("zero points are written only with asym=True")
+    if wq is None:
+        wq = W.new_empty((N, sq_w4_row_bytes(K)), dtype=_U8)
+    if sg is None:
+        sg = W.new_empty((groups, N), dtype=_BF16)
     if asym and zp is None:
-        zp = torch.empty(groups, N, dtype=torch.uint8, device=dev)
+        zp = W.new_empty((groups, N), dtype=_U8)
     _packed("W", wq, sg, zp, (N,), K, group, dev)
     gf = torch.empty_like(gamma) if gamma is not None else None
     bf = torch.empty_like(beta) if beta is not None else None
-    _call("sq_fold_quant_weights_w4", dev, stream, W.data_ptr(), _dt(W), K, N, W.stride(0), _ptr0(s), _ptr0(gamma),
+    _call("sq_fold_quant_weights_w4", dev, stream, W.data_ptr(), dt, K, N, W.stride(0), _ptr0(s), _ptr0(gamma),
           _ptr0(beta), group, wq.data_ptr(), sg.data_ptr(), _ptr0(zp), _ptr0(gf), _ptr0(bf))
     return wq, sg, zp, gf, bf
 
@@ -564,8 +575,8 @@ def sq_w4_dequant(wq: torch.Tensor, sg: torch.Tensor, zp: torch.Tensor | None = 
         raise ValueError("wq must be 2-D")
     N, dev = wq.shape[0], wq.device
     _packed("wq", wq, sg, zp, (N,), K, group, dev)
-    y = _out(y, (N, K), out_dtype, dev)
-    _call("sq_w4_dequant", dev, stream, wq.data_ptr(), sg.data_ptr(), _ptr0(zp), K, N, group, y.data_ptr(), _odt(y),
+    y, ydt = _out(wq, y, (N, K), out_dtype)
+    _call("sq_w4_dequant", dev, stream, wq.data_ptr(), sg.data_ptr(), _ptr0(zp), K, N, group, y.data_ptr(), ydt,
           y.stride(0))
     return y
 
@@ -573,13 +584,13 @@ def sq_w4_dequant(wq: torch.Tensor, sg: torch.Tensor, zp: torch.Tensor | None = 
 def sq_w4_gemm(x: torch.Tensor, wq: torch.Tensor, sg: torch.Tensor, zp: torch.Tensor | None = None, group: int = 128,
                out_dtype: torch.dtype = torch.bfloat16, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y [M, N] = x [M, K] @ values(wq, sg, zp) [N, K]^T, for a few tokens."""
-    x = _mat(x, "x")
+    dt = _float_mat(x, "x")
     M, K = x.shape
     N, dev = wq.shape[0], x.device
     _packed("wq", wq, sg, zp, (N,), K, group, dev)
-    y = _out(y, (M, N), out_dtype, dev)
-    _call("sq_w4_gemm", dev, stream, x.data_ptr(), _dt(x), M, K, x.stride(0), wq.data_ptr(), sg.data_ptr(), _ptr0(zp), N,
-          group, y.data_ptr(), _odt(y), y.stride(0))
+    y, ydt = _out(x, y, (M, N), out_dtype)
+    _call("sq_w4_gemm", dev, stream, x.data_ptr(), dt, M, K, x.stride(0), wq.data_ptr(), sg.data_ptr(), _ptr0(zp), N,
+          group, y.data_ptr(), ydt, y.stride(0))
     return y
 
 
@@ -596,7 +607,7 @@ def sq_moe_w4_workspace(T: int, D: int, F: int, E: int, top_k: int, device="cuda
     return torch.zeros(sq_moe_w4_workspace_size(T, D, F, E, top_k), dtype=torch.uint8, device=device)
 
 
-def _moe(fn, x, E, k, route, w13, s13, w2, s2, z13, z2, group, out_dtype, y, workspace, stream):
+def _moe(fn, x, dt, E, k, route, w13, s13, w2, s2, z13, z2, group, out_dtype, y, workspace, stream):
     T, D = x.shape
     dev = x.device
     if w13.dim() != 3 or w13.shape[1] % 2:
@@ -606,14 +617,14 @@ def _moe(fn, x, E, k, route, w13, s13, w2, s2, z13, z2, group, out_dtype, y, wor
         raise ValueError("zero points are given for both weights or for neither")
     _packed("w13", w13, s13, z13, (E, 2 * F), D, group, dev)
     _packed("w2", w2, s2, z2, (E, D), F, group, dev)
-    y = _out(y, (T, D), out_dtype, dev)
+    y, ydt = _out(x, y, (T, D), out_dtype)
     if workspace is None:
         workspace = sq_moe_w4_workspace(T, D, F, E, k, dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous and on the input's device")
-    _call(fn, dev, stream, x.data_ptr(), _dt(x), T, D, x.stride(0), *route, w13.data_ptr(), s13.data_ptr(), _ptr0(z13),
-          w2.data_ptr(), s2.data_ptr(), _ptr0(z2), F, group, y.data_ptr(), _odt(y), y.stride(0), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+    _call(fn, dev, stream, x.data_ptr(), dt, T, D, x.stride(0), *route, w13.data_ptr(), s13.data_ptr(), _ptr0(z13),
+          w2.data_ptr(), s2.data_ptr(), _ptr0(z2), F, group, y.data_ptr(), ydt, y.stride(0), workspace.data_ptr(),
+          workspace.nbytes)
     return y
 
 
@@ -624,16 +635,15 @@ def sq_moe_w4(x: torch.Tensor, wr: torch.Tensor, top_k: int, w13: torch.Tensor, 
     """A mixture-of-experts layer for a few tokens: router wr [E, D], the top_k experts of each token (softmax
     weights, divided by their sum if renorm), silu(gate) * up, weighted sum.  Returns (y [T, D], ids [T, top_k]
     int32, weights [T, top_k] float32).  workspace: sq_moe_w4_workspace, made for the call if not given."""
-    x = _mat(x, "x")
-    wr = _mat(wr, "wr")
+    dt, rdt = _float_mat(x, "x"), _float_mat(wr, "wr")
     T, E = x.shape[0], wr.shape[0]
     if wr.shape[1] != x.shape[1] or not wr.is_contiguous() or wr.device != x.device:
         raise ValueError("wr must be contiguous [E, D] on the input's device")
     if not 0 < top_k <= E:
         raise ValueError("top_k must be between 1 and the number of experts")
-    ids = torch.empty(T, top_k, dtype=torch.int32, device=x.device)
-    wts = torch.empty(T, top_k, dtype=torch.float32, device=x.device)
-    y = _moe("sq_moe_w4", x, E, top_k, (wr.data_ptr(), _dt(wr), E, top_k, int(renorm), ids.data_ptr(), wts.data_ptr()),
+    ids = x.new_empty((T, top_k), dtype=torch.int32)
+    wts = x.new_empty((T, top_k), dtype=_F32)
+    y = _moe("sq_moe_w4", x, dt, E, top_k, (wr.data_ptr(), rdt, E, top_k, int(renorm), ids.data_ptr(), wts.data_ptr()),
              w13, s13, w2, s2, z13, z2, group, out_dtype, y, workspace, stream)
     return y, ids, wts
 
@@ -644,14 +654,14 @@ def sq_moe_w4_routed(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, 
                      y: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The experts of sq_moe_w4 for given choices: ids [T, top_k] int32 (outside [0, E): left out) and weights
     [T, top_k] float32."""
-    x = _mat(x, "x")
+    dt = _float_mat(x, "x")
     T, E = x.shape[0], w13.shape[0]
     k = ids.shape[-1]
-    for v, dt, name in ((ids, torch.int32, "ids"), (weights, torch.float32, "weights")):
-        if v.dtype != dt or v.shape != (T, k) or not v.is_contiguous() or v.device != x.device:
-            raise ValueError(f"{name} must be contiguous {dt} [T, top_k] on the input's device")
-    return _moe("sq_moe_w4_routed", x, E, k, (ids.data_ptr(), weights.data_ptr(), E, k), w13, s13, w2, s2, z13, z2, group,
-                out_dtype, y, workspace, stream)
+    for v, vdt, name in ((ids, torch.int32, "ids"), (weights, _F32, "weights")):
+        if v.dtype != vdt or v.shape != (T, k) or not v.is_contiguous() or v.device != x.device:
+            raise ValueError(f"{name} must be contiguous {vdt} [T, top_k] on the input's device")
+    return _moe("sq_moe_w4_routed", x, dt, E, k, (ids.data_ptr(), weights.data_ptr(), E, k), w13, s13, w2, s2, z13, z2,
+                group, out_dtype, y, workspace, stream)
 
 
 WAIT_LIMIT_DEFAULT_NS = 10 * 1000 * 1000 * 1000

@@ -720,9 +720,7 @@ cudaError_t launch_experts_t(sqk::MoeParams p, cudaStream_t st) {
   const int64_t slots = (int64_t)p.T * p.top_k, lists = up16(sqk::MoeLists::ints(p.entries, slots) * 4);
   const int64_t rings = std::max(ring, up16(sqk::MoeScratch::bytes(p.E, slots)));  // the lists' scratch comes before
   const int64_t sms = num_sms();
-  auto prepare = [](const void* k) {
-    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBudget);
-  };
+  auto prepare = [](const void* k) { return allow_shared_memory(k, kSmemBudget); };
   // gate and up: as many tiles a pass as a CTA can have, as far as their cells fit beside x, and x in
   // shared memory if half the tiles (at least eight) still have cells
   const int64_t per = ((int64_t)std::min(p.E, p.T * p.top_k) * (p.F / 8) + sms - 1) / sms;

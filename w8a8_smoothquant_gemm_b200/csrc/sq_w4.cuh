@@ -370,3 +370,9 @@ __device__ __forceinline__ void store_out(void* y, int64_t at, float v, bool bf1
 }
 
 }  // namespace sqk
+
+namespace sqh {
+// Lets a kernel of the current device take `bytes` of dynamic shared memory (set once per kernel and device:
+// the call would cost a launch's host time a fair part).
+cudaError_t allow_shared_memory(const void* kern, int64_t bytes);
+}  // namespace sqh

@@ -1,8 +1,11 @@
 // sq_w4_api.cu -- the C ABI of the 4-bit weight operators (include/sq_w8a8.h): argument checks on
 // the host, before any CUDA call, then the launches on the caller's stream.
 #include <climits>
+#include <mutex>
+#include <set>
+#include <utility>
 
-#include "sq_common.cuh"
+#include "sq_w4.cuh"
 
 namespace sqh {
 cudaError_t launch_w4_fold(const void* W, bool bf16, int64_t K, int64_t N, int64_t ldw, const float* s,
@@ -19,6 +22,20 @@ cudaError_t launch_moe_w4(const void* x, bool bf16, int64_t T, int64_t D, int64_
                           const float* wts_in, const uint8_t* w13, const uint16_t* s13, const uint8_t* z13,
                           const uint8_t* w2, const uint16_t* s2, const uint8_t* z2, int64_t F, int group, void* y,
                           bool y_bf16, int64_t ldy, void* workspace, cudaStream_t st);
+
+cudaError_t allow_shared_memory(const void* kern, int64_t bytes) {
+  static std::mutex mu;
+  static std::set<std::pair<int, const void*>> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  const auto key = std::make_pair(dev, kern);
+  if (done.count(key)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.insert(key);
+  return e;
+}
 }  // namespace sqh
 
 namespace {

@@ -216,7 +216,7 @@ cudaError_t launch_w4_gemm_t(sqk::W4GemmParams p, cudaStream_t st) {
   auto kern = sqk::w4_gemm_kernel<NT, S, GW, ASYM, ALIGNED>;
   const int64_t tiles = (p.N + 15) / 16, mt = (p.M + 8 * NT - 1) / (8 * NT);
   const int nu = sqk::w4_units(p.K), mr = std::min(p.M, 8 * NT);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBudget);
+  cudaError_t e = allow_shared_memory((const void*)kern, kSmemBudget);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3(32 * WARPS);
