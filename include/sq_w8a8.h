@@ -375,7 +375,8 @@ sq_status sq_w4_gemm(const void* x, sq_dtype dt, int64_t M, int64_t K, int64_t l
  *   [E, ceil(F / group), D].  z13, z2: zero points shaped like the scales, both or neither.  All
  *   six are 16-byte aligned.
  *   ids: int32 [T, top_k], weights: fp32 [T, top_k], written.  y: [T, D], ldy >= D.
- *   D % 16 == 0, F % 16 == 0, both <= SQ_MAX_K; T <= SQ_MOE_MAX_TOKENS (more: SQ_ERR_UNSUPPORTED).
+ *   D % 16 == 0, F % 16 == 0, both <= SQ_MAX_K, and one expert's W13 and W2 below 4 GiB each;
+ *   T <= SQ_MOE_MAX_TOKENS (more: SQ_ERR_UNSUPPORTED).
  *   workspace: sq_moe_w4_workspace_size(T, D, F, E, top_k) bytes, 256-byte aligned, zero-filled
  *   once before its first use; every call leaves it ready for the next, whatever its sizes.  Calls
  *   that share one must be ordered (on one stream, or by events). */

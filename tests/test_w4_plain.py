@@ -115,7 +115,7 @@ def test_moe_refusals():
     for bad in (dict(x=A8), dict(ldx=260), dict(wr=A8), dict(w13=A8), dict(w2=A8), dict(y=ODD), dict(ids=A2),
                 dict(wts=A2), dict(s13=ODD), dict(s13=A8), dict(s2=A8), dict(z13=A8, z2=A), dict(F=120), dict(D=248, ldx=248), dict(ws=A8)):
         assert moe(**bad) == ALIGN, bad
-    for bad in (dict(T=65), dict(E=1025), dict(E=64, k=33), dict(group=16), dict(F=133152)):
+    for bad in (dict(T=65), dict(E=1025), dict(E=64, k=33), dict(group=16), dict(F=133152), dict(D=131072, ldx=131072, ldy=131072, F=131072)):
         assert moe(**bad) == UNSUPPORTED, bad
     size = sq.sq_moe_w4_workspace_size(4, 256, 128, 8, 2)
     assert moe(ws=None) == WORKSPACE and moe(bytes=size - 1) == WORKSPACE

@@ -23,7 +23,6 @@ namespace sqk {
 constexpr int MOE_MAX_T = 64;    // tokens: one bit each of an expert's token mask
 constexpr int MOE_MAX_E = 1024;  // experts
 constexpr int MOE_MAX_K = 32;    // choices per token
-constexpr int MOE_ENTRY = 32;    // most tokens of an entry: four column tiles of the mma
 
 struct MoeParams {
   const char* x;
@@ -51,6 +50,7 @@ struct MoeParams {
   uint16_t* h;          // [parts, T k, F]
   // the expert kernels' shared memory
   int entries;          // most entries of the lists
+  int entry;            // most tokens of one: 8 a column tile of the mma
   int up_x_at, up_cells_at, up_ring_at, up_pass;  // the lists come first; pass: tiles whose cells fit
   int down_h_at, down_cells_at, down_ring_at, down_pass;
   int C;                // CTAs of the down kernel's cluster
@@ -63,7 +63,7 @@ constexpr int MOE_LOGIT_WARPS = 8;
 constexpr int MOE_RP = 20;  // floats between the down kernel's tokens of a cell: 16 rows, padded to spread the banks
 
 // ---------------------------------------------------------------------------- lists
-// Entries (an expert and up to MOE_ENTRY of its tokens), and slots (a token of an expert), which lie
+// Entries (an expert and up to p.entry of its tokens), and slots (a token of an expert), which lie
 // in the order of the experts and, for one expert, of the tokens.  All in one array of ints, so that
 // the down kernel can copy it as it is.
 struct MoeLists {
@@ -108,7 +108,7 @@ __device__ void moe_build_lists(const MoeParams& p, const MoeLists& l, const Moe
   int mine = 0;
   for (int e = tid * per; e < min(p.E, (tid + 1) * per); ++e) {
     const int c = __popcll(sc.mask[e]);
-    mine += c + ((c + MOE_ENTRY - 1) / MOE_ENTRY << 16);
+    mine += c + ((c + p.entry - 1) / p.entry << 16);
   }
   int sum = mine;
 #pragma unroll
@@ -128,7 +128,7 @@ __device__ void moe_build_lists(const MoeParams& p, const MoeLists& l, const Moe
   for (int e = tid * per; e < min(p.E, (tid + 1) * per); ++e) {
     const int c = __popcll(sc.mask[e]);
     sc.offset[e] = tokens;
-    for (int first = 0; first < c; first += MOE_ENTRY) {
+    for (int first = 0; first < c; first += p.entry) {
       l.expert[active] = e;
       l.start[active] = tokens + first;
       ++active;
@@ -323,7 +323,6 @@ __device__ __forceinline__ void moe_mac(float (&acc)[NTM][4], uint32_t slot, int
     }
   };
   if (NTM == 1 || count <= 8) w4_mac<1, S, GW, ASYM>(acc, slot, lane, x);
-  else if (count <= 16) w4_mac<(NTM > 1 ? 2 : 1), S, GW, ASYM>(acc, slot, lane, x);
   else w4_mac<NTM, S, GW, ASYM>(acc, slot, lane, x);
 }
 
@@ -722,11 +721,11 @@ cudaError_t launch_experts_t(sqk::MoeParams p, cudaStream_t st) {
   const int64_t sms = num_sms();
   auto prepare = [](const void* k) { return allow_shared_memory(k, kSmemBudget); };
   // gate and up: as many tiles a pass as a CTA can have, as far as their cells fit beside x, and x in
-  // shared memory if half the tiles (at least eight) still have cells
+  // shared memory if sixteen tiles still have cells
   const int64_t per = ((int64_t)std::min(p.E, p.T * p.top_k) * (p.F / 8) + sms - 1) / sms;
   const int64_t cell = (int64_t)sqk::w4_cell_floats(NTM) * 4, x = (int64_t)S * p.T * sqk::moe_row_pitch(p.D);
   const bool x_staged =
-      moe_pass(kSmemBudget - lists - rings - x, cell, per) >= std::min<int64_t>(per, std::max<int64_t>(8, per / 2));
+      moe_pass(kSmemBudget - lists - rings - x, cell, per) >= std::min<int64_t>(per, 16);
   p.up_x_at = (int)lists;
   p.up_cells_at = (int)(lists + (x_staged ? x : 0));
   p.up_pass = (int)moe_pass(kSmemBudget - rings - p.up_cells_at, cell, per);
@@ -781,10 +780,11 @@ cudaError_t launch_experts_t(sqk::MoeParams p, cudaStream_t st) {
                           p.C, p, st);
 }
 
+// Entries of 8 tokens (one column tile) where an expert has few on average, else of 16.  An expert with
+// more tokens than an entry is read again for the next, from L2.
 template <int S, int SH, int GW, bool ASYM>
-cudaError_t launch_experts(const sqk::MoeParams& p, cudaStream_t st) {
-  return p.T <= 8 ? launch_experts_t<1, S, SH, GW, ASYM>(p, st)
-                  : launch_experts_t<sqk::MOE_ENTRY / 8, S, SH, GW, ASYM>(p, st);
+cudaError_t launch_experts(sqk::MoeParams p, cudaStream_t st) {
+  return p.entry == 8 ? launch_experts_t<1, S, SH, GW, ASYM>(p, st) : launch_experts_t<2, S, SH, GW, ASYM>(p, st);
 }
 
 template <int S, int SH>
@@ -812,8 +812,8 @@ static size_t moe_layout(sqk::MoeParams* p, char* base, int64_t T, int64_t D, in
     return r;
   };
   sqk::MoeParams q{};
-  // every expert's last entry may be short
-  q.entries = (int)std::min(T * k, E + T * k / sqk::MOE_ENTRY);
+  q.entry = T <= 8 || T * k <= 4 * E ? 8 : 16;
+  q.entries = (int)std::min(T * k, E + T * k / q.entry);  // every expert's last entry may be short
   q.arrived = (unsigned int*)take(8 * sizeof(unsigned int));
   q.logits = (double*)take((size_t)(T * E) * 8);
   q.lists = (int*)take((size_t)sqk::MoeLists::ints(q.entries, T * k) * 4);
@@ -821,6 +821,7 @@ static size_t moe_layout(sqk::MoeParams* p, char* base, int64_t T, int64_t D, in
   q.h = (uint16_t*)take((size_t)(3 * T * k * F) * 2);
   if (p) {
     p->entries = q.entries;
+    p->entry = q.entry;
     p->arrived = q.arrived;
     p->logits = q.logits;
     p->lists = q.lists;

@@ -102,7 +102,10 @@ bool moe_sizes_ok(int64_t T, int64_t D, int64_t F, int64_t E, int64_t top_k) {
   return T >= 0 && D > 0 && F > 0 && E > 0 && top_k > 0 && top_k <= E;
 }
 bool moe_sizes_supported(int64_t T, int64_t D, int64_t F, int64_t E, int64_t top_k) {
-  return T <= SQ_MOE_MAX_TOKENS && E <= SQ_MOE_MAX_EXPERTS && top_k <= SQ_MOE_MAX_TOP_K && D <= SQ_MAX_K && F <= SQ_MAX_K;
+  if (T > SQ_MOE_MAX_TOKENS || E > SQ_MOE_MAX_EXPERTS || top_k > SQ_MOE_MAX_TOP_K || D > SQ_MAX_K || F > SQ_MAX_K)
+    return false;
+  // an expert's codes are reached by 32-bit offsets
+  return 2 * F * sq_w4_row_bytes(D) <= (int64_t)UINT_MAX && D * sq_w4_row_bytes(F) <= (int64_t)UINT_MAX;
 }
 
 sq_status run_moe(const MoeArgs& a, bool routed, void* stream) {
@@ -192,8 +195,7 @@ sq_status sq_w4_gemm(const void* x, sq_dtype dt, int64_t M, int64_t K, int64_t l
   if (st != SQ_OK) return st;
   if (K % 16 != 0 || !aligned(y, elt_size(ydt))) return SQ_ERR_ALIGNMENT;
   if (K > SQ_MAX_K || N > (int64_t)INT_MAX || M > SQ_W4_MAX_M) return SQ_ERR_UNSUPPORTED;
-  if ((K + group - 1) / group * N > (int64_t)UINT_MAX) return SQ_ERR_UNSUPPORTED;  // 32-bit offsets of scales,
-  if (sq_w4_row_bytes(K) > (1ll << 35) / N) return SQ_ERR_UNSUPPORTED;  // and of one block's codes
+  if ((K + group - 1) / group * N > (int64_t)UINT_MAX) return SQ_ERR_UNSUPPORTED;  // 32-bit offsets of scales
   return cuda_status(sqh::launch_w4_gemm(x, dt == SQ_BF16, M, K, ldx, Wq, scales, zeros, N, group, y, ydt == SQ_BF16,
                                          ldy, static_cast<cudaStream_t>(stream)));
 }

@@ -237,6 +237,8 @@ cudaError_t launch_w4_gemm_t(sqk::W4GemmParams p, cudaStream_t st) {
     const int64_t units = (nu + C - 1) / C;
     const bool more = C < 8 && units >= 4;
     p.C = C;
+    // (offsets within a CTA's tiles are 32-bit)
+    const int64_t least = (tiles * 16 * p.w.row_bytes) / (int64_t)(UINT32_MAX - 16 * p.w.row_bytes) + 1;
     p.clusters = (int)std::min<int64_t>(tiles, std::max(sms / C, 1));
     if (C > 1) {
       attr[0].val.clusterDim.x = (unsigned)C;
@@ -249,6 +251,7 @@ cudaError_t launch_w4_gemm_t(sqk::W4GemmParams p, cudaStream_t st) {
       if (e != cudaSuccess) return e;
       p.clusters = (int)std::min<int64_t>(p.clusters, std::max<int64_t>(1, active / mt));
     }
+    p.clusters = (int)std::min(tiles, std::max<int64_t>(p.clusters, least));
     const int64_t per = (tiles + p.clusters - 1) / p.clusters;
     // tiles whose cells fit beside x, the whole of it: all of them, or passes of at least 16
     const int64_t x_all = x_fixed + units * x_unit;
