@@ -285,6 +285,35 @@ __global__ void __launch_bounds__(32 * MOE_LOGIT_WARPS) moe_logits_kernel(const 
 // The lists, by one CTA, from the choices in global memory.
 __device__ __forceinline__ void moe_route(const MoeParams& p, const MoeLists& l, char* scratch, int* warp_sums) {
   const int pairs = p.T * p.top_k;
+  if (p.T == 1) {  // every choice is an entry of its own, in the order of the choices; one warp sees them all
+    if (threadIdx.x < 32) {
+      const int lane = threadIdx.x, e = lane < pairs ? p.ids_in[lane] : -1;
+      const float mine = lane < pairs ? p.wts_in[lane] : 0.0f;
+      const bool valid = e >= 0 && e < p.E;
+      bool first = valid;
+      float w = 0.0f;
+      for (int j = 0; j < pairs; ++j) {
+        const bool same = __shfl_sync(0xffffffffu, e, j) == e;
+        const float v = __shfl_sync(0xffffffffu, mine, j);
+        if (same) w = __fadd_rn(w, v);
+        if (same && j < lane) first = false;
+      }
+      const uint32_t entries = __ballot_sync(0xffffffffu, first);
+      const int at = __popc(entries & ((1u << lane) - 1u)), n = __popc(entries);
+      if (first) {
+        l.expert[at] = e;
+        l.token[at] = 0;
+        l.weight[at] = w;
+      }
+      if (lane <= n) l.start[lane] = lane;
+      if (lane == 0) {
+        *l.active = n;
+        l.start[n] = n;
+      }
+    }
+    __syncthreads();
+    return;
+  }
   const MoeScratch sc(scratch, p.E, pairs);
   for (int i = threadIdx.x; i < pairs; i += MOE_EXPERT_THREADS) {
     sc.ids[i] = p.ids_in[i];
@@ -308,9 +337,10 @@ __global__ void __launch_bounds__(256) moe_split_kernel(const MoeParams p) {
 }
 
 // ---------------------------------------------------------------------------- experts
-// One unit for an entry of `count` <= 8 NTM tokens: as many column tiles as they need.  STAGED: rows are
-// addresses in shared memory, padded with zeros to whole units; else they are read past the caches' help
-// from global memory, `K` values of them.
+// One unit for an entry of `count` <= 8 NTM tokens: as many column tiles as they need, or a single one
+// that holds the parts of x beside each other where they fit (w4_part_column).  STAGED: rows are
+// addresses in shared memory, padded with zeros to whole units; else they are read from global memory,
+// `K` values of them.
 template <bool STAGED, int S, int GW, bool ASYM, int NTM, typename Row>
 __device__ __forceinline__ void moe_mac(float (&acc)[NTM][4], uint32_t slot, int lane, int count,
                                         const Row (&rows)[NTM], int64_t plane, int u, int K) {
@@ -322,8 +352,16 @@ __device__ __forceinline__ void moe_mac(float (&acc)[NTM][4], uint32_t slot, int
       return k < K ? *reinterpret_cast<const uint4*>(rows[n] + s * plane + k * 2) : make_uint4(0, 0, 0, 0);
     }
   };
-  if (NTM == 1 || count <= 8) w4_mac<1, S, GW, ASYM>(acc, slot, lane, x);
+  if (S > 1 && count <= w4_fold_columns(S)) w4_mac<1, 1, GW, ASYM>(acc, slot, lane, x);
+  else if (NTM == 1 || count <= 8) w4_mac<1, S, GW, ASYM>(acc, slot, lane, x);
   else w4_mac<NTM, S, GW, ASYM>(acc, slot, lane, x);
+}
+
+// The row (token of the entry) and part that this lane's column n reads.
+template <int S>
+__device__ __forceinline__ int2 moe_column(int n, int g, int count) {
+  if (S > 1 && count <= w4_fold_columns(S)) return make_int2(min(w4_part_column<S>(g).x, count - 1), w4_part_column<S>(g).y);
+  return make_int2(min(8 * n + g, count - 1), 0);
 }
 
 template <bool STAGED>
@@ -455,8 +493,9 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_up_kernel(const Moe
         count = l.start[a + 1] - s0;
 #pragma unroll
         for (int n = 0; n < NTM; ++n) {
-          const int tok = l.token[s0 + min(8 * n + g, count - 1)];
-          rows[n] = MoeRow<STAGED>::of(smem_u32(xs) + tok * spitch, xbase + tok * xpitch, lane);
+          const int2 col = moe_column<S>(n, g, count);
+          const int tok = l.token[s0 + col.x];
+          rows[n] = MoeRow<STAGED>::of(smem_u32(xs) + (col.y * p.T + tok) * spitch, xbase + tok * xpitch + col.y * xplane, lane);
         }
         begin = false;
       }
@@ -467,6 +506,7 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_up_kernel(const Moe
       spent = slot;
       slot = slot == ring + (MOE_DEPTH - 1) * SLOT ? ring : slot + SLOT;
       if (++b == nb || left == 1) {
+        if (S > 1 && count <= w4_fold_columns(S)) w4_fold<S>(acc[0], lane);
         if (NTM == 1 || count <= 8) w4_put_cell<1>(cell, acc, lane);
         else w4_put_cell<NTM>(cell, acc, lane);
         cell += CELL;
@@ -533,14 +573,6 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_down_kernel(const M
   const int64_t hplane = (int64_t)slots * p.F * 2;
   const int spitch = moe_row_pitch(p.F);
   char* hs = smem + p.down_h_at;  // rows of every slot, part after part
-  if (STAGED) {
-    const int used = l.start[*l.active];
-    for (int s = 0; s < SH; ++s)
-      moe_stage_rows(hs + s * slots * spitch, used, p.F,
-                     [&](int r) { return reinterpret_cast<const char*>(p.h) + s * hplane + (int64_t)r * p.F * 2; });
-  }
-  cp_commit();
-
   for (int p0 = 0; p0 < my_tiles; p0 += p.down_pass) {
     const int n_tiles = min(p.down_pass, my_tiles - p0), line = n_tiles * per_tile;
     if (p0 != 0) __syncthreads();
@@ -588,7 +620,13 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_down_kernel(const M
 #pragma unroll 1
       for (int u = 0; u < MOE_DEPTH - 1; ++u) issue(ring + u * SLOT);
 
-      cp_wait<MOE_DEPTH - 1>();  // h; the ring's units are younger
+      if (STAGED && p0 == 0) {
+        const int used = l.start[*l.active];
+        for (int s = 0; s < SH; ++s)
+          moe_stage_rows(hs + s * slots * spitch, used, p.F,
+                         [&](int r) { return reinterpret_cast<const char*>(p.h) + s * hplane + (int64_t)r * p.F * 2; });
+      }
+      cp_wait_all();  // h, and the ring's first units with it
       __syncthreads();
 
       float acc[NTM][4] = {};
@@ -608,9 +646,11 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_down_kernel(const M
 #pragma unroll
           for (int n = 0; n < NTM; ++n)
             {
-              const int row = s0 + min(8 * n + g, count - 1);
-              rows[n] = MoeRow<STAGED>::of(smem_u32(hs) + row * spitch,
-                                           reinterpret_cast<const char*>(p.h) + (int64_t)row * p.F * 2, lane);
+              const int2 col = moe_column<SH>(n, g, count);
+              const int row = s0 + col.x;
+              rows[n] = MoeRow<STAGED>::of(smem_u32(hs) + (col.y * slots + row) * spitch,
+                                           reinterpret_cast<const char*>(p.h) + col.y * hplane + (int64_t)row * p.F * 2,
+                                           lane);
             }
           begin = false;
         }
@@ -622,6 +662,7 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_down_kernel(const M
         slot = slot == ring + (MOE_DEPTH - 1) * SLOT ? ring : slot + SLOT;
         ++at;
         if (++b == nb || at == per_tile || left == 1) {
+          if (count <= w4_fold_columns(SH)) w4_fold<SH>(acc[0], lane);
 #pragma unroll
           for (int n = 0; n < NTM; ++n) {
 #pragma unroll

@@ -175,6 +175,9 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // What a lane copies of the next unit.
 struct W4Cursor {
   const char *lo, *hi;  // its 16 bytes of rows g and g + 8
@@ -275,6 +278,29 @@ __device__ __forceinline__ void w4_mac(float (&acc)[NTA][4], uint32_t slot, int 
 #pragma unroll
         for (int n = 0; n < NT; ++n) w4_scale_add(acc[n], slo, shi, tmp[n]);
       }
+    }
+  }
+}
+
+// Few columns whose x has S parts need not take S products: the parts can be columns of one product
+// beside each other.  Column g of 8 is then part g / C of column g % C (C = 4 for two parts, 2 for
+// three), and the sums of a column's parts are added at the end.
+__host__ __device__ constexpr int w4_fold_columns(int S) { return S == 2 ? 4 : S == 3 ? 2 : 0; }
+template <int S>
+__device__ __forceinline__ int2 w4_part_column(int g) {
+  constexpr int C = S == 2 ? 4 : 2;
+  return make_int2(g % C, min(g / C, S - 1));
+}
+// Adds the parts; the lanes of columns below C have the sums.
+template <int S>
+__device__ __forceinline__ void w4_fold(float (&acc)[4], int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (S == 2) {
+      acc[i] = __fadd_rn(acc[i], __shfl_xor_sync(0xffffffffu, acc[i], 2));
+    } else {
+      const float b = __shfl_sync(0xffffffffu, acc[i], (lane & ~3) | 1), c = __shfl_sync(0xffffffffu, acc[i], (lane & ~3) | 2);
+      acc[i] = __fadd_rn(acc[i], __fadd_rn(b, c));
     }
   }
 }

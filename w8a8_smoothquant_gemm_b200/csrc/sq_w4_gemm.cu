@@ -74,6 +74,8 @@ __global__ void __launch_bounds__(32 * W4G_WARPS, 1) w4_gemm_kernel(const W4Gemm
   uint32_t xs[NT];                       // this lane's columns (addresses); absent tokens read the last one
 #pragma unroll
   for (int n = 0; n < NT; ++n) xs[n] = smem_u32(smem) + min(8 * n + g, Mr - 1) * pitch + t * 16;
+  const bool fold = S > 1 && NT == 1 && Mr <= w4_fold_columns(S);  // the parts of x beside each other
+  if (fold) xs[0] = smem_u32(smem) + (w4_part_column<S>(g).y * Mr + min(w4_part_column<S>(g).x, Mr - 1)) * pitch + t * 16;
   const int plane = Mr * pitch;
   const bool whole = p.chunk >= b1 - b0;
 
@@ -153,13 +155,15 @@ __global__ void __launch_bounds__(32 * W4G_WARPS, 1) w4_gemm_kernel(const W4Gemm
             cp_wait<DEPTH - 2>();
             __syncwarp();
             issue(spent);
-            w4_mac<NT, S, GW, ASYM>(acc, slot, lane,
-                                    [&](int k, int s, int w) { return lds128(xs[k] + xo + s * plane + w * 64); });
+            auto x = [&](int k, int s, int w) { return lds128(xs[k] + xo + s * plane + w * 64); };
+            if (S > 1 && NT == 1 && fold) w4_mac<1, 1, GW, ASYM>(acc, slot, lane, x);
+            else w4_mac<NT, S, GW, ASYM>(acc, slot, lane, x);
             spent = slot;
             slot = slot == ring + (DEPTH - 1) * SLOT ? ring : slot + SLOT;
             xo += 2 * W4_UNIT;
           }
           {  // the end of this warp's part of the tile
+            if (S > 1 && NT == 1 && fold) w4_fold<S>(acc[0], lane);
             w4_put_cell<NT>(cell, acc, lane);
             cell += CELL;
 #pragma unroll
