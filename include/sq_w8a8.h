@@ -326,8 +326,8 @@ int64_t sq_w4_row_bytes(int64_t K);
 
 /* sq_fold_quant_weights_w4 -- sq_fold_quant_weights with 4-bit group-wise weights:
  *   W'[j, n] = s_j * W[j, n]   (s may be NULL: W' = W)
- *   zeros == NULL: scale = bf16(max|W'| / 7), code = 8 + clamp(rne(W' / scale), -7, 7)
- *   zeros != NULL: lo = min(0, min W'), hi = max(0, max W'), scale = bf16((hi - lo) / 15),
+ *   zeros == NULL: scale = bf16(max|W'| * RN(1/7)), code = 8 + clamp(rne(W' / scale), -7, 7)
+ *   zeros != NULL: lo = min(0, min W'), hi = max(0, max W'), scale = bf16((hi - lo) * RN(1/15)),
  *                  zero = clamp(rne(-lo / scale), 0, 15), code = clamp(rne(W' / scale) + zero, 0, 15)
  *   over the group's channels j; a zero scale gives the code 8 (zeros == NULL) or zero point and
  *   code 0.  Wq: [N, sq_w4_row_bytes(K)] bytes, 16-byte aligned.  W must be finite.  K % 16 == 0,

@@ -86,6 +86,21 @@ def test_fold_without_factors_and_with_a_padded_matrix():
     assert np.array_equal(a[0].cpu().numpy(), P.pack(P.quantise(W, None, 64, False)[0]))
 
 
+@pytest.mark.parametrize("zero", range(16))
+def test_fold_rounds_ties_to_even_codes_before_the_zero_point(zero):
+    """A grid of step 1/16 with each zero point, and values on every half step of it."""
+    W = np.zeros((64, 8), np.float32)
+    W[:, :] = (np.arange(64)[:, None] % 31) * 0.5 - zero
+    W = np.clip(W, -zero, 15 - zero) / 16
+    wq, sg, zp, _, _ = sq.sq_fold_quant_weights_w4(dev(W), group=64, asym=True)
+    codes, r_sg, r_zp = P.quantise(W, None, 64, True)
+    assert (r_sg == 1 / 16).all() and (r_zp == zero).all()
+    assert np.array_equal(zp.cpu().numpy(), r_zp) and np.array_equal(wq.cpu().numpy(), P.pack(codes))
+    half = W * 16 % 1 == 0.5
+    assert half.sum() > 100 and (codes.T[half].astype(int) - zero).astype(int).tolist() == np.clip(
+        np.rint(W[half] * 16), -zero, 15 - zero).astype(int).tolist()
+
+
 def test_fold_extreme_magnitudes():
     """Scales far outside the range of the shared reciprocal, and ones that round to zero."""
     rng = np.random.default_rng(4)

@@ -57,9 +57,9 @@ def quantise(W, s, group, asym):
         v = w[k0:k0 + group]
         if asym:
             lo, hi = np.minimum(v.min(0), f(0)), np.maximum(v.max(0), f(0))
-            sc = bf16((hi - lo) / f(15))
+            sc = bf16((hi - lo) * (f(1) / f(15)))
         else:
-            sc = bf16(np.abs(v).max(0) / f(7))
+            sc = bf16(np.abs(v).max(0) * (f(1) / f(7)))
         d = np.where(sc == 0, f(1), sc)
         q = np.where(sc == 0, f(0), np.rint(v / d))
         if asym:

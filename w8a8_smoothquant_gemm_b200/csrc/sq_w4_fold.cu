@@ -4,9 +4,9 @@
 // Quantiser ("量化：只压权重，与训练后量化（PTQ）": group-wise round to nearest; "SmoothQuant大模型
 // 平滑量化技术", Python demo: max / largest code, round, clip), every operation one binary32 rounding:
 //   W' = s_j W[j, n]
-//   symmetric:        scale = bf16(max|W'| / 7),               code = 8 + clamp(rne(W' / scale), -7, 7)
+//   symmetric:        scale = bf16(max|W'| * RN(1/7)),         code = 8 + clamp(rne(W' / scale), -7, 7)
 //   with zero points: lo = min(0, min W'), hi = max(0, max W'),
-//                     scale = bf16((hi - lo) / 15), zero = clamp(rne(-lo / scale), 0, 15),
+//                     scale = bf16((hi - lo) * RN(1/15)), zero = clamp(rne(-lo / scale), 0, 15),
 //                     code = clamp(rne(W' / scale) + zero, 0, 15)
 // A zero scale gives codes equal to the zero point.  The scale is rounded to bf16 before the codes
 // are taken, so the rounding costs no accuracy beyond the grid's own: codes are nearest on the grid
@@ -27,7 +27,7 @@ constexpr int W4F_THREADS = 256;    // 32 column pairs x 2 format blocks x 4 wor
 constexpr int W4F_PITCH = 128 + 16; // bytes per staged code row (16-byte aligned, spreads the banks)
 
 template <bool BF16, bool ASYM>
-__global__ void __launch_bounds__(W4F_THREADS)
+__global__ void __launch_bounds__(W4F_THREADS, BF16 ? 3 : 2)
 w4_fold_kernel(const char* __restrict__ W, int64_t K, int64_t N, int64_t ld_bytes, const float* __restrict__ s,
                const float* __restrict__ gamma, const float* __restrict__ beta, int gw, int groups, int64_t row_bytes,
                char* __restrict__ wq, uint16_t* __restrict__ sg, uint8_t* __restrict__ zp, float* __restrict__ gamma_f,
@@ -41,15 +41,24 @@ w4_fold_kernel(const char* __restrict__ W, int64_t K, int64_t N, int64_t ld_byte
   const int rows = n < N ? (int)max((int64_t)0, min((int64_t)32, K - k0)) : 0;  // rows are whole 16-byte
   const char* src = W + k0 * ld_bytes + n * (BF16 ? 2 : 4);                     // vectors: N is even
   uint32_t raw[BF16 ? 32 : 64];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
+  auto read = [&](int i, const char* at) {
     if (BF16) {
-      raw[i] = i < rows ? __ldg(reinterpret_cast<const uint32_t*>(src + i * ld_bytes)) : 0u;
+      raw[i] = __ldg(reinterpret_cast<const uint32_t*>(at));
     } else {
-      const uint2 v = i < rows ? __ldg(reinterpret_cast<const uint2*>(src + i * ld_bytes)) : make_uint2(0u, 0u);
-      raw[2 * i] = v.x;
-      raw[2 * i + 1] = v.y;
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
+      raw[BF16 ? 0 : 2 * i] = v.x;
+      raw[BF16 ? 0 : 2 * i + 1] = v.y;
     }
+  };
+  if (rows == 32) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i, src += ld_bytes) read(i, src);
+  } else {
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 32 : 64); ++i) raw[i] = 0u;
+#pragma unroll
+    for (int i = 0; i < 32; ++i, src += ld_bytes)
+      if (i < rows) read(i, src);
   }
   {
     const int64_t k = u0 + tid;
@@ -61,21 +70,21 @@ w4_fold_kernel(const char* __restrict__ W, int64_t K, int64_t N, int64_t ld_byte
     }
   }
   __syncthreads();
-  float2 v[32];
+  // W' of row i (bf16: from the bits each time, which keeps the registers at half; the product is one
+  // operation for two channels)
+  auto value = [&](int i, float f) {
+    const float2 a = BF16 ? make_float2(bf16lo(raw[i]), bf16hi(raw[i]))
+                          : make_float2(__uint_as_float(raw[BF16 ? 0 : 2 * i]), __uint_as_float(raw[BF16 ? 0 : 2 * i + 1]));
+    return __fmul2_rn(make_float2(f, f), a);
+  };
   float2 top = make_float2(0.0f, 0.0f), bot = top;  // for symmetric scales, top is the largest magnitude
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
     const float4 f = *reinterpret_cast<const float4*>(factor + 32 * col + i);
-    const float fi[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 a = BF16 ? make_float2(bf16lo(raw[i + j]), bf16hi(raw[i + j]))
-                            : make_float2(__uint_as_float(raw[BF16 ? 0 : 2 * (i + j)]), __uint_as_float(raw[BF16 ? 0 : 2 * (i + j) + 1]));
-      v[i + j] = __fmul2_rn(make_float2(fi[j], fi[j]), a);
-    }
+    const float2 v[4] = {value(i, f.x), value(i + 1, f.y), value(i + 2, f.z), value(i + 3, f.w)};
 #pragma unroll
     for (int j = 0; j < 4; j += 2) {
-      const float2 p = v[i + j], q = v[i + j + 1];
+      const float2 p = v[j], q = v[j + 1];
       if (ASYM) {
         top = make_float2(fmax3(top.x, p.x, q.x), fmax3(top.y, p.y, q.y));
         bot = make_float2(-fmax3(-bot.x, -p.x, -q.x), -fmax3(-bot.y, -p.y, -q.y));
@@ -98,8 +107,9 @@ w4_fold_kernel(const char* __restrict__ W, int64_t K, int64_t N, int64_t ld_byte
       }
     }
   }
-  const float2 range = ASYM ? make_float2(__fdiv_rn(__fsub_rn(top.x, bot.x), 15.0f), __fdiv_rn(__fsub_rn(top.y, bot.y), 15.0f))
-                            : make_float2(__fdiv_rn(top.x, 7.0f), __fdiv_rn(top.y, 7.0f));
+  const float per = ASYM ? 1.0f / 15.0f : 1.0f / 7.0f;
+  const float2 range = ASYM ? make_float2(__fmul_rn(__fsub_rn(top.x, bot.x), per), __fmul_rn(__fsub_rn(top.y, bot.y), per))
+                            : make_float2(__fmul_rn(top.x, per), __fmul_rn(top.y, per));
   const __nv_bfloat16 sb[2] = {__float2bfloat16_rn(range.x), __float2bfloat16_rn(range.y)};
   const float2 scale = make_float2(__bfloat162float(sb[0]), __bfloat162float(sb[1]));
   float2 zero = make_float2(8.0f, 8.0f);
@@ -110,25 +120,32 @@ w4_fold_kernel(const char* __restrict__ W, int64_t K, int64_t N, int64_t ld_byte
   const SharedDivisor dx(scale.x), dy(scale.y);
   uint32_t wx[4], wy[4];
   if (dx.fast && dy.fast) {
-    // Adding 1.5 * 2^23 + zero rounds the quotient to an integer, ties to even, and leaves the code
-    // in the low bits of the sum (0x4b400000 + code).  The quotient lies within 1 + 2^-8 (the scale's
-    // rounding to bf16) of the codes' range: below 7.03 of a symmetric grid's 7.5, and never below
-    // rne(lo / scale) = -zero; only the upper end of a grid with a zero point can need the clip.
-    const float2 rc = make_float2(dx.y, dy.y), nb = make_float2(-dx.b, -dy.b);
-    const float2 magic = make_float2(12582912.0f + zero.x, 12582912.0f + zero.y);
+    // Adding 1.5 * 2^23 rounds the quotient q to an integer, ties to even, and leaves it in the low bits
+    // of the sum (0x4b400000 + q).  Shifted sums of eight are a word of codes after one correction: their
+    // exponents and leading bits (the larger shifts push them out), and the zero point in every nibble.
+    // q lies within 1 + 2^-8 (the scale's rounding to bf16) of the codes' range: below 7.03 of a symmetric
+    // grid's 7.5, and never below rne(lo / scale) = -zero; only the upper end of a grid with a zero point
+    // can need the clip.
+    constexpr uint32_t excess = 0x4b400000u + (0x4b400000u << 4) + (0x4b400000u << 8);
+    const uint32_t fixx = (uint32_t)(int)zero.x * 0x11111111u - excess, fixy = (uint32_t)(int)zero.y * 0x11111111u - excess;
+    const float2 rc = make_float2(dx.y, dy.y), nb = make_float2(-dx.b, -dy.b), magic = make_float2(12582912.0f, 12582912.0f);
+    const float2 most = make_float2(12582927.0f - zero.x, 12582927.0f - zero.y);
 #pragma unroll
     for (int i = 0; i < 32; i += 8) {
       uint32_t ax = 0u, ay = 0u;
+      const float4 fa = *reinterpret_cast<const float4*>(factor + 32 * col + i);
+      const float4 fb = *reinterpret_cast<const float4*>(factor + 32 * col + i + 4);
+      const float f[8] = {fa.x, fa.y, fa.z, fa.w, fb.x, fb.y, fb.z, fb.w};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        float2 t = __fadd2_rn(markstein2(v[i + j], rc, nb), magic);
-        if (ASYM) t = make_float2(fminf(t.x, 12582927.0f), fminf(t.y, 12582927.0f));
+        float2 t = __fadd2_rn(markstein2(value(i + j, f[j]), rc, nb), magic);
+        if (ASYM) t = make_float2(fminf(t.x, most.x), fminf(t.y, most.y));
         const int sh = 4 * (j / 2) + 16 * (j % 2);
-        ax += (__float_as_uint(t.x) - 0x4b400000u) << sh;
-        ay += (__float_as_uint(t.y) - 0x4b400000u) << sh;
+        ax += __float_as_uint(t.x) << sh;
+        ay += __float_as_uint(t.y) << sh;
       }
-      wx[i / 8] = ax;
-      wy[i / 8] = ay;
+      wx[i / 8] = ax + fixx;
+      wy[i / 8] = ay + fixy;
     }
   } else {  // rare: a scale outside the fast range (its rounding to bf16 may then be coarse)
 #pragma unroll
@@ -137,7 +154,8 @@ w4_fold_kernel(const char* __restrict__ W, int64_t K, int64_t N, int64_t ld_byte
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int sh = 4 * (j / 2) + 16 * (j % 2);
-        const float qx = rintf(dx.div(v[i + j].x)), qy = rintf(dy.div(v[i + j].y));
+        const float2 v = value(i + j, factor[32 * col + i + j]);
+        const float qx = rintf(dx.div(v.x)), qy = rintf(dy.div(v.y));
         const float cx = ASYM ? fminf(fmaxf(__fadd_rn(qx, zero.x), 0.0f), 15.0f) : fminf(fmaxf(qx, -7.0f), 7.0f) + 8.0f;
         const float cy = ASYM ? fminf(fmaxf(__fadd_rn(qy, zero.y), 0.0f), 15.0f) : fminf(fmaxf(qy, -7.0f), 7.0f) + 8.0f;
         ax |= (uint32_t)(int)cx << sh;
@@ -174,44 +192,71 @@ w4_fold_kernel(const char* __restrict__ W, int64_t K, int64_t N, int64_t ld_byte
   }
 }
 
+constexpr int W4D_THREADS = 128, W4D_ROWS = W4D_THREADS / 32 * 4;
+
 // Values: (code - zero) * scale, at most 12 significant bits (exact in binary32), rounded once for
-// bf16.  One thread per 16 bytes of codes: four runs of 8 consecutive k.  A warp takes 32 pieces of
-// one row, so both sides are whole lines.
+// bf16.  A thread takes 16 bytes of codes (four runs of 8 consecutive k) of four rows, so that four
+// loads are on their way and the rows' scales come together; a warp takes 32 pieces of each row, so both
+// sides are whole lines.  Bound by the values' bytes.
 template <bool BF16>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(W4D_THREADS, 6)
 w4_dequant_kernel(const char* __restrict__ wq, const uint16_t* __restrict__ sg, const uint8_t* __restrict__ zp, int K,
-                  int64_t N, int gw, int row_bytes, char* __restrict__ y, int64_t ld_bytes) {
+                  int64_t N, int gw, int row_bytes, char* __restrict__ y, int64_t ld_bytes, bool together) {
   const int piece = blockIdx.x * 32 + threadIdx.x % 32, b = piece / 4, t = piece % 4;
   if (piece * 16 >= row_bytes) return;
-  for (int64_t n = (int64_t)blockIdx.y * 8 + threadIdx.x / 32; n < N; n += (int64_t)gridDim.y * 8) {
-    const uint4 c = ldg_stream16(wq + n * row_bytes + piece * 16);
-    const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+  for (int64_t n0 = (int64_t)blockIdx.y * W4D_ROWS + threadIdx.x / 32 * 4; n0 < N; n0 += (int64_t)gridDim.y * W4D_ROWS) {
+    uint4 c[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      c[r] = n0 + r < N ? ldg_stream16(wq + (n0 + r) * row_bytes + piece * 16) : make_uint4(0u, 0u, 0u, 0u);
+    uint2 s = make_uint2(0u, 0u);
+    uint32_t z = 0x08080808u;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       const int k = b * W4_BLOCK + 32 * w + 8 * t;
       if (k >= K) continue;
-      const int64_t g = (int64_t)(b * (4 / gw) + w / gw) * N + n;
-      const float scale = __uint_as_float((uint32_t)__ldg(sg + g) << 16);
-      // 2^23 + code, minus 2^23 + zero: exact
-      const float zero = 8388608.0f + (zp ? (float)__ldg(zp + g) : 8.0f);
-      float f[8];
+      if (w % gw == 0) {  // the four rows' scales and zero points of this group
+        const int64_t g = (int64_t)(b * (4 / gw) + w / gw) * N + n0;
+        if (together) {
+          s = __ldg(reinterpret_cast<const uint2*>(sg + g));
+          if (zp) z = __ldg(reinterpret_cast<const uint32_t*>(zp + g));
+        } else {
+          uint32_t v[4] = {0u, 0u, 0u, 0u}, q[4] = {8u, 8u, 8u, 8u};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t code = (word[w] >> (4 * (e / 2) + 16 * (e % 2))) & 15u;
-        f[e] = __fmul_rn(__fsub_rn(__uint_as_float(0x4b000000u | code), zero), scale);
-      }
-      char* out = y + n * ld_bytes + (int64_t)k * (BF16 ? 2 : 4);
-      if (BF16) {
-        uint32_t o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
-          o[e] = *reinterpret_cast<const uint32_t*>(&h);
+          for (int r = 0; r < 4; ++r)
+            if (n0 + r < N) {
+              v[r] = __ldg(sg + g + r);
+              if (zp) q[r] = __ldg(zp + g + r);
+            }
+          s = make_uint2(v[0] | (v[1] << 16), v[2] | (v[3] << 16));
+          z = q[0] | (q[1] << 8) | (q[2] << 16) | (q[3] << 24);
         }
-        __stcs(reinterpret_cast<uint4*>(out), make_uint4(o[0], o[1], o[2], o[3]));
-      } else {
-        __stcs(reinterpret_cast<float4*>(out), make_float4(f[0], f[1], f[2], f[3]));
-        __stcs(reinterpret_cast<float4*>(out + 16), make_float4(f[4], f[5], f[6], f[7]));
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (n0 + r >= N) continue;
+        const uint32_t word = w == 0 ? c[r].x : w == 1 ? c[r].y : w == 2 ? c[r].z : c[r].w;
+        const float scale = r % 2 ? bf16hi(r < 2 ? s.x : s.y) : bf16lo(r < 2 ? s.x : s.y);
+        const float zero = __uint_as_float(0x4b000000u | ((z >> (8 * r)) & 0xffu));  // 2^23 + zero
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t code = (word >> (4 * (e / 2) + 16 * (e % 2))) & 15u;
+          f[e] = __fmul_rn(__fsub_rn(__uint_as_float(0x4b000000u | code), zero), scale);
+        }
+        char* out = y + (n0 + r) * ld_bytes + (int64_t)k * (BF16 ? 2 : 4);
+        if (BF16) {
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+            o[e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          __stcs(reinterpret_cast<uint4*>(out), make_uint4(o[0], o[1], o[2], o[3]));
+        } else {
+          __stcs(reinterpret_cast<float4*>(out), make_float4(f[0], f[1], f[2], f[3]));
+          __stcs(reinterpret_cast<float4*>(out + 16), make_float4(f[4], f[5], f[6], f[7]));
+        }
       }
     }
   }
@@ -239,9 +284,11 @@ cudaError_t launch_w4_fold(const void* W, bool bf16, int64_t K, int64_t N, int64
 cudaError_t launch_w4_dequant(const uint8_t* wq, const uint16_t* sg, const uint8_t* zp, int64_t K, int64_t N, int group,
                               void* y, bool y_bf16, int64_t ldy, cudaStream_t st) {
   const int row_bytes = (int)(sqk::w4_blocks(K) * sqk::W4_BLOCK_BYTES);
-  const dim3 grid((unsigned)((row_bytes / 16 + 31) / 32), (unsigned)std::min<int64_t>((N + 7) / 8, 65535));
+  const dim3 grid((unsigned)((row_bytes / 16 + 31) / 32), (unsigned)std::min<int64_t>((N + sqk::W4D_ROWS - 1) / sqk::W4D_ROWS, 65535));
+  const bool together = N % 4 == 0 && (uintptr_t)sg % 8 == 0 && (uintptr_t)zp % 4 == 0;
   auto go = [&](auto kern) {
-    kern<<<grid, 256, 0, st>>>((const char*)wq, sg, zp, (int)K, N, group / 32, row_bytes, (char*)y, ldy * (y_bf16 ? 2 : 4));
+    kern<<<grid, sqk::W4D_THREADS, 0, st>>>((const char*)wq, sg, zp, (int)K, N, group / 32, row_bytes, (char*)y, ldy * (y_bf16 ? 2 : 4),
+                            together);
   };
   y_bf16 ? go(sqk::w4_dequant_kernel<true>) : go(sqk::w4_dequant_kernel<false>);
   return cudaGetLastError();
