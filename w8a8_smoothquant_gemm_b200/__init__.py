@@ -467,29 +467,27 @@ def sq_selfcheck_shared_divisor(a: torch.Tensor, b: torch.Tensor, want_quotients
 # A packed weight is (wq [N, sq_w4_row_bytes(K)] uint8, sg [ceil(K / group), N] bfloat16, zp uint8
 # like sg or None); experts stack these on a leading dimension.  Calls run on the tensors' own
 # device: its current stream is taken unless `stream` is given.  In decode a call's host time
-# counts, so what can be wrong is looked at in few steps and named in a second look.
+# counts, so the checks are few steps where everything is right; what is wrong is found out after.
 def sq_w4_row_bytes(K: int) -> int:
     return (K + 127) // 128 * 64
 
 
-_BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
+_BF16, _F32, _U8, _I32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
 _FDT = {_BF16: SQ_BF16, _F32: SQ_F32}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _call(fn: str, dev: torch.device, stream, *args):
-    """One library call on `dev`, made the current device for it if it is not."""
-    if dev.type != "cuda":
-        raise ValueError("expected CUDA tensors")
+def _call(fn: str, dev: int, stream, *args):
+    """One library call on device `dev`, made the current one for it if it is not."""
     if stream is None:
-        raw = _raw_stream(dev.index)
-    elif stream.device != dev:
+        raw = _raw_stream(dev)
+    elif stream.device_index != dev:
         raise ValueError("the stream belongs to another device than the tensors")
     else:
         raw = stream.cuda_stream
     f = getattr(_lib or lib(), fn)
-    if dev.index == _current_device():
+    if dev == _current_device():
         status = f(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -507,17 +505,23 @@ def _float_mat(t: torch.Tensor, name: str) -> int:
     return dt
 
 
-def _packed(name: str, wq, sg, zp, lead: tuple, K: int, group: int, dev):
+def _same(t, shape: tuple, dtype, dev: int) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+
+
+def _check_packed(name: str, wq, sg, zp, lead: tuple, K: int, group: int, dev: int):
     """Checks one packed weight: codes [*lead, row bytes], scales (and zero points) [.., groups, N]."""
     if group not in (32, 64, 128):
         raise ValueError("group must be 32, 64 or 128")
-    gshape = (*lead[:-1], (K + group - 1) // group, lead[-1])
-    if wq.shape != (*lead, (K + 127) // 128 * 64) or wq.dtype is not _U8 or not wq.is_contiguous() or wq.device != dev:
-        raise ValueError(f"{name}: codes must be contiguous uint8 {(*lead, sq_w4_row_bytes(K))} on the input's device")
-    if sg.shape != gshape or sg.dtype is not _BF16 or not sg.is_contiguous() or sg.device != dev:
-        raise ValueError(f"{name}: scales must be contiguous bfloat16 {gshape} on the input's device")
-    if zp is not None and (zp.shape != gshape or zp.dtype is not _U8 or not zp.is_contiguous() or zp.device != dev):
-        raise ValueError(f"{name}: zero points must be contiguous uint8 {gshape} on the input's device")
+    codes, scales = (*lead, sq_w4_row_bytes(K)), (*lead[:-1], -(-K // group), lead[-1])
+    if dev < 0:
+        raise ValueError("expected CUDA tensors")
+    if not _same(wq, codes, _U8, dev):
+        raise ValueError(f"{name}: codes must be contiguous uint8 {codes} on the input's device")
+    if not _same(sg, scales, _BF16, dev):
+        raise ValueError(f"{name}: scales must be contiguous bfloat16 {scales} on the input's device")
+    if zp is not None and not _same(zp, scales, _U8, dev):
+        raise ValueError(f"{name}: zero points must be contiguous uint8 {scales} on the input's device")
 
 
 def _ptr0(t):
@@ -543,24 +547,26 @@ def sq_fold_quant_weights_w4(W: torch.Tensor, s: torch.Tensor | None = None, gam
     """W [K, N] -> (wq packed, sg, zp or None, gamma / s or None, beta / s or None).  asym: with zero points."""
     dt = _float_mat(W, "W")
     K, N = W.shape
-    dev = W.device
+    dev = W.get_device()
     for v, name in ((s, "s"), (gamma, "gamma"), (beta, "beta")):
         if v is not None:
             _vec(v, K, name)
-            if v.device != dev:
+            if v.get_device() != dev:
                 raise ValueError(f"{name} must be on W's device")
     if group not in (32, 64, 128):
         raise ValueError("group must be 32, 64 or 128")
-    groups = (K + group - 1) // group
     if not asym and zp is not None:
         raise ValueError("zero points are written only with asym=True")
+    given = wq is not None or sg is not None or zp is not None
+    groups = -(-K // group)
     if wq is None:
         wq = W.new_empty((N, sq_w4_row_bytes(K)), dtype=_U8)
     if sg is None:
         sg = W.new_empty((groups, N), dtype=_BF16)
     if asym and zp is None:
         zp = W.new_empty((groups, N), dtype=_U8)
-    _packed("W", wq, sg, zp, (N,), K, group, dev)
+    if given:
+        _check_packed("W", wq, sg, zp, (N,), K, group, dev)
     gf = torch.empty_like(gamma) if gamma is not None else None
     bf = torch.empty_like(beta) if beta is not None else None
     _call("sq_fold_quant_weights_w4", dev, stream, W.data_ptr(), dt, K, N, W.stride(0), _ptr0(s), _ptr0(gamma),
@@ -573,9 +579,9 @@ def sq_w4_dequant(wq: torch.Tensor, sg: torch.Tensor, zp: torch.Tensor | None = 
     """The values [N, K] that a packed weight stands for: (code - zero) * scale."""
     if wq.dim() != 2:
         raise ValueError("wq must be 2-D")
-    N, dev = wq.shape[0], wq.device
-    _packed("wq", wq, sg, zp, (N,), K, group, dev)
-    y, ydt = _out(wq, y, (N, K), out_dtype)
+    N, dev = wq.shape[0], wq.get_device()
+    _check_packed("wq", wq, sg, zp, (N,), K, group, dev)
+    y, ydt = _out(sg, y, (N, K), out_dtype)
     _call("sq_w4_dequant", dev, stream, wq.data_ptr(), sg.data_ptr(), _ptr0(zp), K, N, group, y.data_ptr(), ydt,
           y.stride(0))
     return y
@@ -586,11 +592,11 @@ def sq_w4_gemm(x: torch.Tensor, wq: torch.Tensor, sg: torch.Tensor, zp: torch.Te
     """y [M, N] = x [M, K] @ values(wq, sg, zp) [N, K]^T, for a few tokens."""
     dt = _float_mat(x, "x")
     M, K = x.shape
-    N, dev = wq.shape[0], x.device
-    _packed("wq", wq, sg, zp, (N,), K, group, dev)
+    N, dev = wq.shape[0], x.get_device()
+    _check_packed("wq", wq, sg, zp, (N,), K, group, dev)
     y, ydt = _out(x, y, (M, N), out_dtype)
-    _call("sq_w4_gemm", dev, stream, x.data_ptr(), dt, M, K, x.stride(0), wq.data_ptr(), sg.data_ptr(), _ptr0(zp), N,
-          group, y.data_ptr(), ydt, y.stride(0))
+    _call("sq_w4_gemm", dev, stream, x.data_ptr(), dt, M, K, x.stride(0), wq.data_ptr(), sg.data_ptr(),
+          None if zp is None else zp.data_ptr(), N, group, y.data_ptr(), ydt, y.stride(0))
     return y
 
 
@@ -609,18 +615,18 @@ def sq_moe_w4_workspace(T: int, D: int, F: int, E: int, top_k: int, device="cuda
 
 def _moe(fn, x, dt, E, k, route, w13, s13, w2, s2, z13, z2, group, out_dtype, y, workspace, stream):
     T, D = x.shape
-    dev = x.device
+    dev = x.get_device()
     if w13.dim() != 3 or w13.shape[1] % 2:
         raise ValueError("w13 must be [E, 2 F, row bytes]")
     F = w13.shape[1] // 2
     if (z13 is None) != (z2 is None):
         raise ValueError("zero points are given for both weights or for neither")
-    _packed("w13", w13, s13, z13, (E, 2 * F), D, group, dev)
-    _packed("w2", w2, s2, z2, (E, D), F, group, dev)
+    _check_packed("w13", w13, s13, z13, (E, 2 * F), D, group, dev)
+    _check_packed("w2", w2, s2, z2, (E, D), F, group, dev)
     y, ydt = _out(x, y, (T, D), out_dtype)
     if workspace is None:
-        workspace = sq_moe_w4_workspace(T, D, F, E, k, dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
+        workspace = sq_moe_w4_workspace(T, D, F, E, k, x.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous and on the input's device")
     _call(fn, dev, stream, x.data_ptr(), dt, T, D, x.stride(0), *route, w13.data_ptr(), s13.data_ptr(), _ptr0(z13),
           w2.data_ptr(), s2.data_ptr(), _ptr0(z2), F, group, y.data_ptr(), ydt, y.stride(0), workspace.data_ptr(),
@@ -637,11 +643,11 @@ def sq_moe_w4(x: torch.Tensor, wr: torch.Tensor, top_k: int, w13: torch.Tensor, 
     int32, weights [T, top_k] float32).  workspace: sq_moe_w4_workspace, made for the call if not given."""
     dt, rdt = _float_mat(x, "x"), _float_mat(wr, "wr")
     T, E = x.shape[0], wr.shape[0]
-    if wr.shape[1] != x.shape[1] or not wr.is_contiguous() or wr.device != x.device:
+    if wr.shape[1] != x.shape[1] or not wr.is_contiguous() or wr.get_device() != x.get_device():
         raise ValueError("wr must be contiguous [E, D] on the input's device")
     if not 0 < top_k <= E:
         raise ValueError("top_k must be between 1 and the number of experts")
-    ids = x.new_empty((T, top_k), dtype=torch.int32)
+    ids = x.new_empty((T, top_k), dtype=_I32)
     wts = x.new_empty((T, top_k), dtype=_F32)
     y = _moe("sq_moe_w4", x, dt, E, top_k, (wr.data_ptr(), rdt, E, top_k, int(renorm), ids.data_ptr(), wts.data_ptr()),
              w13, s13, w2, s2, z13, z2, group, out_dtype, y, workspace, stream)
@@ -655,11 +661,9 @@ def sq_moe_w4_routed(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, 
     """The experts of sq_moe_w4 for given choices: ids [T, top_k] int32 (outside [0, E): left out) and weights
     [T, top_k] float32."""
     dt = _float_mat(x, "x")
-    T, E = x.shape[0], w13.shape[0]
-    k = ids.shape[-1]
-    for v, vdt, name in ((ids, torch.int32, "ids"), (weights, _F32, "weights")):
-        if v.dtype != vdt or v.shape != (T, k) or not v.is_contiguous() or v.device != x.device:
-            raise ValueError(f"{name} must be contiguous {vdt} [T, top_k] on the input's device")
+    T, E, k, dev = x.shape[0], w13.shape[0], ids.shape[-1], x.get_device()
+    if not _same(ids, (T, k), _I32, dev) or not _same(weights, (T, k), _F32, dev):
+        raise ValueError("ids must be contiguous int32 and weights contiguous float32 [T, top_k], on the input's device")
     return _moe("sq_moe_w4_routed", x, dt, E, k, (ids.data_ptr(), weights.data_ptr(), E, k), w13, s13, w2, s2, z13, z2,
                 group, out_dtype, y, workspace, stream)
 

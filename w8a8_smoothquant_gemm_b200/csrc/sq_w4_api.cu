@@ -29,11 +29,15 @@ cudaError_t allow_shared_memory(const void* kern, int64_t bytes) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lock(mu);
-  const auto key = std::make_pair(dev, kern);
-  if (done.count(key)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) done.insert(key);
+  try {
+    std::lock_guard<std::mutex> lock(mu);
+    const auto key = std::make_pair(dev, kern);
+    if (done.count(key)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.insert(key);
+  } catch (...) {  // out of host memory, or a lock that cannot be taken: no exception leaves a C entry
+    return cudaErrorMemoryAllocation;
+  }
   return e;
 }
 }  // namespace sqh

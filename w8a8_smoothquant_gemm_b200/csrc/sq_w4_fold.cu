@@ -32,6 +32,7 @@ w4_fold_kernel(const char* __restrict__ W, int64_t K, int64_t N, int64_t ld_byte
                const float* __restrict__ gamma, const float* __restrict__ beta, int gw, int groups, int64_t row_bytes,
                char* __restrict__ wq, uint16_t* __restrict__ sg, uint8_t* __restrict__ zp, float* __restrict__ gamma_f,
                float* __restrict__ beta_f) {
+  wait_for_previous_kernel();
   __shared__ float2 ext[2][8][W4F_COLS / 2];  // extremes of each 32-code column, by column pair
   __shared__ __align__(16) float factor[W4_UNIT];
   __shared__ __align__(16) char codes[W4F_COLS * W4F_PITCH];
@@ -202,6 +203,7 @@ template <bool BF16>
 __global__ void __launch_bounds__(W4D_THREADS, 6)
 w4_dequant_kernel(const char* __restrict__ wq, const uint16_t* __restrict__ sg, const uint8_t* __restrict__ zp, int K,
                   int64_t N, int gw, int row_bytes, char* __restrict__ y, int64_t ld_bytes, bool together) {
+  wait_for_previous_kernel();
   const int piece = blockIdx.x * 32 + threadIdx.x % 32, b = piece / 4, t = piece % 4;
   if (piece * 16 >= row_bytes) return;
   for (int64_t n0 = (int64_t)blockIdx.y * W4D_ROWS + threadIdx.x / 32 * 4; n0 < N; n0 += (int64_t)gridDim.y * W4D_ROWS) {
@@ -265,6 +267,25 @@ w4_dequant_kernel(const char* __restrict__ wq, const uint16_t* __restrict__ sg, 
 }  // namespace sqk
 
 namespace sqh {
+namespace {
+
+// A launch that may begin before the previous kernel on the stream is done (the kernels wait for it), which
+// also costs the host less than one without the attribute.
+struct Dependent {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  Dependent(dim3 grid, unsigned threads, cudaStream_t st) {
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+  }
+};
+
+}  // namespace
 
 cudaError_t launch_w4_fold(const void* W, bool bf16, int64_t K, int64_t N, int64_t ldw, const float* s,
                            const float* gamma, const float* beta, int group, uint8_t* wq, uint16_t* sg, uint8_t* zp,
@@ -272,13 +293,13 @@ cudaError_t launch_w4_fold(const void* W, bool bf16, int64_t K, int64_t N, int64
   const int64_t row_bytes = sqk::w4_blocks(K) * sqk::W4_BLOCK_BYTES, ldb = ldw * (bf16 ? 2 : 4);
   const int gw = group / 32, groups = (int)((K + group - 1) / group);
   const dim3 grid((unsigned)((N + sqk::W4F_COLS - 1) / sqk::W4F_COLS), (unsigned)sqk::w4_units(K));
+  Dependent launch(grid, sqk::W4F_THREADS, st);
   auto go = [&](auto kern) {
-    kern<<<grid, sqk::W4F_THREADS, 0, st>>>((const char*)W, K, N, ldb, s, gamma, beta, gw, groups, row_bytes,
-                                            (char*)wq, sg, zp, gamma_f, beta_f);
+    return cudaLaunchKernelEx(&launch.cfg, kern, (const char*)W, K, N, ldb, s, gamma, beta, gw, groups, row_bytes,
+                              (char*)wq, sg, zp, gamma_f, beta_f);
   };
-  if (bf16) zp ? go(sqk::w4_fold_kernel<true, true>) : go(sqk::w4_fold_kernel<true, false>);
-  else zp ? go(sqk::w4_fold_kernel<false, true>) : go(sqk::w4_fold_kernel<false, false>);
-  return cudaGetLastError();
+  if (bf16) return zp ? go(sqk::w4_fold_kernel<true, true>) : go(sqk::w4_fold_kernel<true, false>);
+  return zp ? go(sqk::w4_fold_kernel<false, true>) : go(sqk::w4_fold_kernel<false, false>);
 }
 
 cudaError_t launch_w4_dequant(const uint8_t* wq, const uint16_t* sg, const uint8_t* zp, int64_t K, int64_t N, int group,
@@ -286,12 +307,12 @@ cudaError_t launch_w4_dequant(const uint8_t* wq, const uint16_t* sg, const uint8
   const int row_bytes = (int)(sqk::w4_blocks(K) * sqk::W4_BLOCK_BYTES);
   const dim3 grid((unsigned)((row_bytes / 16 + 31) / 32), (unsigned)std::min<int64_t>((N + sqk::W4D_ROWS - 1) / sqk::W4D_ROWS, 65535));
   const bool together = N % 4 == 0 && (uintptr_t)sg % 8 == 0 && (uintptr_t)zp % 4 == 0;
+  Dependent launch(grid, sqk::W4D_THREADS, st);
   auto go = [&](auto kern) {
-    kern<<<grid, sqk::W4D_THREADS, 0, st>>>((const char*)wq, sg, zp, (int)K, N, group / 32, row_bytes, (char*)y, ldy * (y_bf16 ? 2 : 4),
-                            together);
+    return cudaLaunchKernelEx(&launch.cfg, kern, (const char*)wq, sg, zp, (int)K, N, group / 32, row_bytes, (char*)y,
+                              ldy * (y_bf16 ? 2 : 4), together);
   };
-  y_bf16 ? go(sqk::w4_dequant_kernel<true>) : go(sqk::w4_dequant_kernel<false>);
-  return cudaGetLastError();
+  return y_bf16 ? go(sqk::w4_dequant_kernel<true>) : go(sqk::w4_dequant_kernel<false>);
 }
 
 }  // namespace sqh
