@@ -236,6 +236,29 @@ def test_two_streams_with_a_workspace_each():
     assert all(torch.equal(y, w) for y, w in zip(ys, want))
 
 
+def test_what_a_call_allocates_belongs_to_its_stream():
+    """The current stream is busy while calls on two others make their own workspaces and choices, which are
+    dropped at once: a zero-fill left to the current stream, or memory passed from one stream to the other,
+    would show."""
+    L = Layer(13, 16, 512, 256, 128, False, "bf16")
+    xd, wr = [dev(L.x(8), "bf16") for _ in range(2)], dev(L.wr, "bf16")
+    want = [sq.sq_moe_w4(a, wr, 4, *L.weights(), **L.kw()) for a in xd]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # some 50 ms
+    ys = []
+    for _ in range(20):
+        ys.append([sq.sq_moe_w4(a, wr, 4, *L.weights(), **L.kw(), stream=st)[0] for a, st in zip(xd, streams)])
+    for st in streams:
+        st.synchronize()
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, w[0]) for pair in ys for y, w in zip(pair, want))
+    torch.cuda._sleep(100_000_000)
+    routed = sq.sq_moe_w4_routed(xd[0], want[0][1], want[0][2], *L.weights(), **L.kw(), stream=streams[0])
+    streams[0].synchronize()
+    assert torch.equal(routed, want[0][0])
+
+
 def test_experts_past_32_bit_offsets():
     """2.7 GB of gate and up codes; only the last experts are named."""
     E, D, F = 80, 4096, 8192

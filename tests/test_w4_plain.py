@@ -143,6 +143,20 @@ def test_moe_workspace_size():
             sq.sq_moe_w4_workspace_size(*bad)
 
 
+def test_moe_workspace_serves_smaller_sizes():
+    """The size grows with every argument, also where the experts' lists change their shape."""
+    size = sq.sq_moe_w4_workspace_size
+    for E in (1, 2, 5, 8, 15, 33, 128):
+        for k in (1, 2, 5, 8, 15, 32):
+            if k > E:
+                continue
+            of_T = [size(T, 16, 16, E, k) for T in range(1, 65)]
+            assert of_T == sorted(of_T)
+            for T in (1, 7, 8, 9, 16, 33, 64):
+                assert size(T, 16, 16, E, k) <= size(T, 16, 16, E + 1, k)
+                assert k in (E, 32) or size(T, 16, 16, E, k) <= size(T, 16, 16, E, k + 1)
+
+
 def test_binding_refuses_what_the_call_could_not_see():
     """Shapes, types and devices: checked before a pointer is taken."""
     x = torch.zeros(2, 256, dtype=torch.bfloat16)

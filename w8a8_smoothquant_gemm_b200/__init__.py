@@ -466,7 +466,8 @@ def sq_selfcheck_shared_divisor(a: torch.Tensor, b: torch.Tensor, want_quotients
 # ----------------------------------------------------------------------------- 4-bit weights
 # A packed weight is (wq [N, sq_w4_row_bytes(K)] uint8, sg [ceil(K / group), N] bfloat16, zp uint8
 # like sg or None); experts stack these on a leading dimension.  Calls run on the tensors' own
-# device: its current stream is taken unless `stream` is given.  In decode a call's host time
+# device: its current stream is taken unless `stream` is given, and what a call allocates (outputs,
+# a workspace and its zeros) belongs to the stream it runs on.  In decode a call's host time
 # counts, so the checks are few steps where everything is right; what is wrong is found out after.
 def sq_w4_row_bytes(K: int) -> int:
     return (K + 127) // 128 * 64
@@ -478,15 +479,16 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _call(fn: str, dev: int, stream, *args):
-    """One library call on device `dev`, made the current one for it if it is not."""
-    if stream is None:
-        raw = _raw_stream(dev)
-    elif stream.device_index != dev:
+def _on(stream, like: torch.Tensor):
+    """The context of a call on `stream`: it is the current one while the call allocates and launches."""
+    if stream.device_index != like.get_device():
         raise ValueError("the stream belongs to another device than the tensors")
-    else:
-        raw = stream.cuda_stream
-    f = getattr(_lib or lib(), fn)
+    return torch.cuda.stream(stream)
+
+
+def _call(fn: str, dev: int, *args):
+    """One library call on the current stream of device `dev`, made the current one for it if it is not."""
+    f, raw = getattr(_lib or lib(), fn), _raw_stream(dev)
     if dev == _current_device():
         status = f(*args, raw)
     else:
@@ -545,6 +547,9 @@ def sq_fold_quant_weights_w4(W: torch.Tensor, s: torch.Tensor | None = None, gam
                              wq: torch.Tensor | None = None, sg: torch.Tensor | None = None,
                              zp: torch.Tensor | None = None, stream=None):
     """W [K, N] -> (wq packed, sg, zp or None, gamma / s or None, beta / s or None).  asym: with zero points."""
+    if stream is not None:
+        with _on(stream, W):
+            return sq_fold_quant_weights_w4(W, s, gamma, beta, group, asym, wq, sg, zp)
     dt = _float_mat(W, "W")
     K, N = W.shape
     dev = W.get_device()
@@ -569,7 +574,7 @@ def sq_fold_quant_weights_w4(W: torch.Tensor, s: torch.Tensor | None = None, gam
         _check_packed("W", wq, sg, zp, (N,), K, group, dev)
     gf = torch.empty_like(gamma) if gamma is not None else None
     bf = torch.empty_like(beta) if beta is not None else None
-    _call("sq_fold_quant_weights_w4", dev, stream, W.data_ptr(), dt, K, N, W.stride(0), _ptr0(s), _ptr0(gamma),
+    _call("sq_fold_quant_weights_w4", dev, W.data_ptr(), dt, K, N, W.stride(0), _ptr0(s), _ptr0(gamma),
           _ptr0(beta), group, wq.data_ptr(), sg.data_ptr(), _ptr0(zp), _ptr0(gf), _ptr0(bf))
     return wq, sg, zp, gf, bf
 
@@ -577,12 +582,15 @@ def sq_fold_quant_weights_w4(W: torch.Tensor, s: torch.Tensor | None = None, gam
 def sq_w4_dequant(wq: torch.Tensor, sg: torch.Tensor, zp: torch.Tensor | None = None, *, K: int, group: int = 128,
                   out_dtype: torch.dtype = torch.bfloat16, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The values [N, K] that a packed weight stands for: (code - zero) * scale."""
+    if stream is not None:
+        with _on(stream, wq):
+            return sq_w4_dequant(wq, sg, zp, K=K, group=group, out_dtype=out_dtype, y=y)
     if wq.dim() != 2:
         raise ValueError("wq must be 2-D")
     N, dev = wq.shape[0], wq.get_device()
     _check_packed("wq", wq, sg, zp, (N,), K, group, dev)
     y, ydt = _out(sg, y, (N, K), out_dtype)
-    _call("sq_w4_dequant", dev, stream, wq.data_ptr(), sg.data_ptr(), _ptr0(zp), K, N, group, y.data_ptr(), ydt,
+    _call("sq_w4_dequant", dev, wq.data_ptr(), sg.data_ptr(), _ptr0(zp), K, N, group, y.data_ptr(), ydt,
           y.stride(0))
     return y
 
@@ -590,12 +598,15 @@ def sq_w4_dequant(wq: torch.Tensor, sg: torch.Tensor, zp: torch.Tensor | None = 
 def sq_w4_gemm(x: torch.Tensor, wq: torch.Tensor, sg: torch.Tensor, zp: torch.Tensor | None = None, group: int = 128,
                out_dtype: torch.dtype = torch.bfloat16, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y [M, N] = x [M, K] @ values(wq, sg, zp) [N, K]^T, for a few tokens."""
+    if stream is not None:
+        with _on(stream, x):
+            return sq_w4_gemm(x, wq, sg, zp, group, out_dtype, y)
     dt = _float_mat(x, "x")
     M, K = x.shape
     N, dev = wq.shape[0], x.get_device()
     _check_packed("wq", wq, sg, zp, (N,), K, group, dev)
     y, ydt = _out(x, y, (M, N), out_dtype)
-    _call("sq_w4_gemm", dev, stream, x.data_ptr(), dt, M, K, x.stride(0), wq.data_ptr(), sg.data_ptr(),
+    _call("sq_w4_gemm", dev, x.data_ptr(), dt, M, K, x.stride(0), wq.data_ptr(), sg.data_ptr(),
           None if zp is None else zp.data_ptr(), N, group, y.data_ptr(), ydt, y.stride(0))
     return y
 
@@ -613,7 +624,7 @@ def sq_moe_w4_workspace(T: int, D: int, F: int, E: int, top_k: int, device="cuda
     return torch.zeros(sq_moe_w4_workspace_size(T, D, F, E, top_k), dtype=torch.uint8, device=device)
 
 
-def _moe(fn, x, dt, E, k, route, w13, s13, w2, s2, z13, z2, group, out_dtype, y, workspace, stream):
+def _moe(fn, x, dt, E, k, route, w13, s13, w2, s2, z13, z2, group, out_dtype, y, workspace):
     T, D = x.shape
     dev = x.get_device()
     if w13.dim() != 3 or w13.shape[1] % 2:
@@ -628,7 +639,7 @@ def _moe(fn, x, dt, E, k, route, w13, s13, w2, s2, z13, z2, group, out_dtype, y,
         workspace = sq_moe_w4_workspace(T, D, F, E, k, x.device)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous and on the input's device")
-    _call(fn, dev, stream, x.data_ptr(), dt, T, D, x.stride(0), *route, w13.data_ptr(), s13.data_ptr(), _ptr0(z13),
+    _call(fn, dev, x.data_ptr(), dt, T, D, x.stride(0), *route, w13.data_ptr(), s13.data_ptr(), _ptr0(z13),
           w2.data_ptr(), s2.data_ptr(), _ptr0(z2), F, group, y.data_ptr(), ydt, y.stride(0), workspace.data_ptr(),
           workspace.nbytes)
     return y
@@ -641,6 +652,9 @@ def sq_moe_w4(x: torch.Tensor, wr: torch.Tensor, top_k: int, w13: torch.Tensor, 
     """A mixture-of-experts layer for a few tokens: router wr [E, D], the top_k experts of each token (softmax
     weights, divided by their sum if renorm), silu(gate) * up, weighted sum.  Returns (y [T, D], ids [T, top_k]
     int32, weights [T, top_k] float32).  workspace: sq_moe_w4_workspace, made for the call if not given."""
+    if stream is not None:
+        with _on(stream, x):
+            return sq_moe_w4(x, wr, top_k, w13, s13, w2, s2, z13, z2, group, renorm, out_dtype, y, workspace)
     dt, rdt = _float_mat(x, "x"), _float_mat(wr, "wr")
     T, E = x.shape[0], wr.shape[0]
     if wr.shape[1] != x.shape[1] or not wr.is_contiguous() or wr.get_device() != x.get_device():
@@ -650,7 +664,7 @@ def sq_moe_w4(x: torch.Tensor, wr: torch.Tensor, top_k: int, w13: torch.Tensor, 
     ids = x.new_empty((T, top_k), dtype=_I32)
     wts = x.new_empty((T, top_k), dtype=_F32)
     y = _moe("sq_moe_w4", x, dt, E, top_k, (wr.data_ptr(), rdt, E, top_k, int(renorm), ids.data_ptr(), wts.data_ptr()),
-             w13, s13, w2, s2, z13, z2, group, out_dtype, y, workspace, stream)
+             w13, s13, w2, s2, z13, z2, group, out_dtype, y, workspace)
     return y, ids, wts
 
 
@@ -660,12 +674,15 @@ def sq_moe_w4_routed(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, 
                      y: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The experts of sq_moe_w4 for given choices: ids [T, top_k] int32 (outside [0, E): left out) and weights
     [T, top_k] float32."""
+    if stream is not None:
+        with _on(stream, x):
+            return sq_moe_w4_routed(x, ids, weights, w13, s13, w2, s2, z13, z2, group, out_dtype, y, workspace)
     dt = _float_mat(x, "x")
     T, E, k, dev = x.shape[0], w13.shape[0], ids.shape[-1], x.get_device()
     if not _same(ids, (T, k), _I32, dev) or not _same(weights, (T, k), _F32, dev):
         raise ValueError("ids must be contiguous int32 and weights contiguous float32 [T, top_k], on the input's device")
     return _moe("sq_moe_w4_routed", x, dt, E, k, (ids.data_ptr(), weights.data_ptr(), E, k), w13, s13, w2, s2, z13, z2,
-                group, out_dtype, y, workspace, stream)
+                group, out_dtype, y, workspace)
 
 
 WAIT_LIMIT_DEFAULT_NS = 10 * 1000 * 1000 * 1000

@@ -5,7 +5,7 @@
 //   y[t]         = sum over the chosen e of weight[t, e] * (W2_e h[t, e])
 //
 // Bound: the chosen experts' codes, each read once from HBM.  Three kernels, chained as
-// programmatic dependents: router logits; choice, gate and up; down.  The work is cut by (expert,
+// programmatic dependents: router and choice; gate and up; down.  The work is cut by (expert,
 // rows), never by token: an expert's weights are read once for all of its tokens, which are the
 // columns of the mma (sq_w4.cuh).
 //   Router sums are binary64, so that which experts are chosen does not hang on rounding.  The last
@@ -28,7 +28,6 @@ struct MoeParams {
   const char* x;
   int64_t ldx_bytes;
   const char* wr;
-  int x_bf16, wr_bf16;
   int T, D, F, E, top_k, renorm;
   int* ids;
   float* wts;
@@ -45,9 +44,9 @@ struct MoeParams {
   // workspace
   unsigned int* arrived;  // [8] router blocks that are done with 8 tokens; wrap to 0 by themselves
   double* logits;         // [T, E]
-  int* lists;           // see MoeLists
-  uint16_t* xparts;     // [3, T, D] (binary32 x)
-  uint16_t* h;          // [parts, T k, F]
+  int* lists;             // see MoeLists
+  uint16_t* xparts;       // [3, T, D] (binary32 x)
+  uint16_t* h;            // [parts, T k, F]
   // the expert kernels' shared memory
   int entries;          // most entries of the lists
   int entry;            // most tokens of one: 8 a column tile of the mma
@@ -543,7 +542,7 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_up_kernel(const Moe
   }
 }
 
-// Down: a tile is 16 rows d; its blocks are those of every entry in turn (a rank of a cluster takes
+// Down: a tile is 16 rows d; its units are those of every entry in turn (a rank of a cluster takes
 // a share of that line, where there are few tiles).  A cell holds sums for every token, to which an
 // entry's are added with the tokens' weights when the warp leaves the entry.
 template <bool STAGED, int NTM, int SH, int GW, bool ASYM>
@@ -578,7 +577,7 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_down_kernel(const M
     if (p0 != 0) __syncthreads();
     if (line > 0) {
       const W4Run run = w4_runs<MOE_WARPS>(runs, line, per_tile, warp, lane);
-        int tile = run.tile, at = run.b;  // block of the tile's line
+      int tile = run.tile, at = run.b;  // unit of the tile's line
       int a = (first + at) / nb, b = first + at - a * nb;
       float* cell = cells + run.cell * cell_floats;
 
@@ -586,7 +585,7 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_down_kernel(const M
       base.row_bytes = (uint32_t)p.rb2;
       base.pitch = p.D;
       base.groups = p.g2;
-        auto place = [&](int ti, int entry, int at_b) {
+      auto place = [&](int ti, int entry, int at_b) {
         const int64_t e = l.expert[entry];
         base.codes = p.w2 + e * p.D * p.rb2;
         base.scales = p.s2 + e * p.g2 * p.D;
@@ -644,14 +643,13 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_down_kernel(const M
           s0 = l.start[a];
           count = l.start[a + 1] - s0;
 #pragma unroll
-          for (int n = 0; n < NTM; ++n)
-            {
-              const int2 col = moe_column<SH>(n, g, count);
-              const int row = s0 + col.x;
-              rows[n] = MoeRow<STAGED>::of(smem_u32(hs) + (col.y * slots + row) * spitch,
-                                           reinterpret_cast<const char*>(p.h) + col.y * hplane + (int64_t)row * p.F * 2,
-                                           lane);
-            }
+          for (int n = 0; n < NTM; ++n) {
+            const int2 col = moe_column<SH>(n, g, count);
+            const int row = s0 + col.x;
+            rows[n] = MoeRow<STAGED>::of(smem_u32(hs) + (col.y * slots + row) * spitch,
+                                         reinterpret_cast<const char*>(p.h) + col.y * hplane + (int64_t)row * p.F * 2,
+                                         lane);
+          }
           begin = false;
         }
         cp_wait<MOE_DEPTH - 2>();
@@ -857,7 +855,8 @@ static size_t moe_layout(sqk::MoeParams* p, char* base, int64_t T, int64_t D, in
   q.entries = (int)std::min(T * k, E + T * k / q.entry);  // every expert's last entry may be short
   q.arrived = (unsigned int*)take(8 * sizeof(unsigned int));
   q.logits = (double*)take((size_t)(T * E) * 8);
-  q.lists = (int*)take((size_t)sqk::MoeLists::ints(q.entries, T * k) * 4);
+  // (room for entries of 8 in any case, so that the size grows with each of its arguments)
+  q.lists = (int*)take((size_t)sqk::MoeLists::ints(std::min(T * k, E + T * k / 8), T * k) * 4);
   q.xparts = (uint16_t*)take((size_t)(3 * T * D) * 2);
   q.h = (uint16_t*)take((size_t)(3 * T * k * F) * 2);
   if (p) {
@@ -887,8 +886,6 @@ cudaError_t launch_moe_w4(const void* x, bool bf16, int64_t T, int64_t D, int64_
   p.x = (const char*)x;
   p.ldx_bytes = ldx * (bf16 ? 2 : 4);
   p.wr = (const char*)wr;
-  p.x_bf16 = bf16;
-  p.wr_bf16 = wr_bf16;
   p.T = (int)T;
   p.D = (int)D;
   p.F = (int)F;

@@ -12,8 +12,6 @@
 //     mma's packed operands want them: one shift and one three-input logic operation a pair.
 #pragma once
 
-#include <cuda_fp16.h>
-
 #include "sq_ptx.cuh"
 
 namespace sqk {
@@ -174,9 +172,7 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-
 __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // What a lane copies of the next unit.
 struct W4Cursor {

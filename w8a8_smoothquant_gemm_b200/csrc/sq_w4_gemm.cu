@@ -3,14 +3,14 @@
 // y[m, n] = sum_g scale[g, n] * sum_{k in g} (code[n, k] - zero[g, n]) * x[m, k]
 //
 // Bound: the weight codes' K N / 2 bytes from HBM; at a few tokens every other term is small.  So
-// the codes go from memory to registers once, with 16-byte loads kept several blocks ahead, and
-// are turned into bf16 operands there (exact small integers).  The products run on mma.sync: its
+// the codes go from memory through a small ring in shared memory to registers once, copied
+// asynchronously a unit ahead (sq_w4.cuh), and are turned into bf16 operands there (exact small integers).  The products run on mma.sync: its
 // operands are registers, which is where the codes are unpacked, and at M <= 8 one 16 x 8 x 16
 // step consumes 256 weights, so the tensor pipe is far from its limit (tcgen05 would want the
 // unpacked operand written to shared memory first, four times the bytes of the codes).
 //
 // One CTA per SM (or cluster of CTAs, which then cut K between them because there are few rows or
-// x is long) owns a run of 16-row tiles.  Its (tile, block) list is cut into 16 equal runs, one a
+// x is long) owns a run of 16-row tiles.  Its list of (tile, unit) is cut into 16 equal runs, one a
 // warp, whatever the sizes; a warp streams its run through its ring without a pause (sq_w4.cuh).
 // x is staged in shared memory once, as bf16 parts (one for bf16, three for binary32, which together
 // are x exactly); where it does not fit it comes in chunks of K.  A warp's sum over its part of a
@@ -139,13 +139,13 @@ __global__ void __launch_bounds__(32 * W4G_WARPS, 1) w4_gemm_kernel(const W4Gemm
                              part[4][s] | (part[5][s] << 16), part[6][s] | (part[7][s] << 16));
           }
         }
-        cp_wait<DEPTH - 1>();  // x; the ring's blocks are younger
+        cp_wait<DEPTH - 1>();  // x; the ring's units are younger
         __syncthreads();
 
         float acc[NT][4];
 #pragma unroll
         for (int k = 0; k < NT; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.0f;
-        uint32_t slot = ring, spent = ring + (DEPTH - 1) * SLOT;  // the next block's, the last one's
+        uint32_t slot = ring, spent = ring + (DEPTH - 1) * SLOT;  // the next unit's, the last one's
         uint32_t xo = b * (2 * W4_UNIT);
         while (left > 0) {
           const int part = min(left, units - b);  // of the tile
