@@ -167,6 +167,136 @@ def test_gemm_many_channels_for_few_tokens(M, group, asym, dt):
     check(sq.sq_w4_gemm(dev(x, dt), wq, sg, zp, group=group, out_dtype=torch.float32), ref, bound, "f32")
 
 
+@pytest.mark.parametrize("M", [9, 16, 17, 31, 32, 33, 64, 65, 130])
+@pytest.mark.parametrize("K,N,group,asym,dt", [(16, 8, 128, False, "bf16"), (128, 136, 32, True, "bf16"),
+                                               (400, 128, 64, True, "bf16"), (1040, 1000, 64, False, "f32"),
+                                               (2064, 4104, 128, True, "bf16"), (272, 40, 32, True, "f32"),
+                                               (4096, 520, 32, True, "bf16"), (8192, 264, 128, False, "f32")])
+def test_gemm_for_a_batch(M, K, N, group, asym, dt):
+    """Nine tokens and more, whole pieces of scales: last units of one block, last tiles of few channels, blocks of
+    tokens that are not full, K over clusters."""
+    rng = np.random.default_rng(M * K + N)
+    (wq, sg, zp), w = random_weight(rng, K, N, group, asym)
+    x = activations(rng, M, K, dt)
+    ref, bound = P.product(x, w, group)
+    for out in ("bf16", "f32"):
+        y = sq.sq_w4_gemm(dev(x, dt), wq, sg, zp, group=group, out_dtype=TD[out])
+        check(y, ref, bound, out)
+        assert torch.equal(y, sq.sq_w4_gemm(dev(x, dt), wq, sg, zp, group=group, out_dtype=TD[out]))
+
+
+@pytest.mark.parametrize("M", [12, 24, 48])
+@pytest.mark.parametrize("K,N,group,asym,dt", [(2048, 50000, 64, True, "bf16"), (1040, 30008, 128, False, "f32"),
+                                               (256, 60000, 32, False, "bf16")])
+def test_gemm_for_a_batch_many_tiles(M, K, N, group, asym, dt):
+    """Many tiles to a CTA: every ring, buffer and barrier goes round several times."""
+    rng = np.random.default_rng(M + K + N)
+    (wq, sg, zp), w = random_weight(rng, K, N, group, asym)
+    x = activations(rng, M, K, dt)
+    ref, bound = P.product(x, w, group)
+    check(sq.sq_w4_gemm(dev(x, dt), wq, sg, zp, group=group, out_dtype=torch.float32), ref, bound, "f32")
+
+
+@pytest.mark.parametrize("M", [9, 20, 64])
+def test_gemm_for_a_batch_is_exact_on_integers(M):
+    rng = np.random.default_rng(M)
+    K, N = 1296, 2056
+    codes = rng.integers(0, 16, (N, K)).astype(np.uint8)
+    sg = (2.0 ** rng.integers(-3, 4, (-(-K // 64), N))).astype(np.float32)
+    zp = rng.integers(0, 16, sg.shape).astype(np.uint8)
+    wq = P.pack(codes)
+    x = rng.integers(-8, 9, (M, K)).astype(np.float32)
+    ref = x.astype(np.float64) @ P.values(wq, sg, zp, K, 64).T
+    for dt in ("bf16", "f32"):
+        y = sq.sq_w4_gemm(dev(x, dt), dev(wq), dev(sg).to(torch.bfloat16), dev(zp), group=64, out_dtype=torch.float32)
+        assert np.array_equal(num(y), ref)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_gemm_for_a_batch_strides_infinities_and_the_rows_behind(dt):
+    rng = np.random.default_rng(13)
+    M, K, N = 21, 400, 264
+    codes = rng.integers(9, 16, (N, K)).astype(np.uint8)  # positive weights only
+    sg = P.bf16(rng.uniform(0.5, 2, (4, N)).astype(np.float32))
+    wq = P.pack(codes)
+    w = P.values(wq, sg, None, K, 128)
+    x = activations(rng, M, K, dt)
+    x[1, 399], x[2, 0], x[4, 200] = np.inf, np.nan, -np.inf
+    wide = torch.full((M + 1, K + 32), float("nan"), dtype=TD[dt], device=DEV)
+    wide[:M, 16:K + 16] = dev(x, dt)
+    y = torch.full((M + 2, N + 5), -7.0, device=DEV)
+    sq.sq_w4_gemm(wide[:M, 16:K + 16], dev(wq), dev(sg).to(torch.bfloat16), y=y[1:M + 1, 3:N + 3])
+    got = num(y[1:M + 1, 3:N + 3])
+    assert (got[1] == np.inf).all() and np.isnan(got[2]).all() and (got[4] == -np.inf).all()
+    rows = [m for m in range(M) if m not in (1, 2, 4)]
+    ref, bound = P.product(x[rows], w, 128)
+    assert (np.abs(got[rows] - ref) <= bound + np.abs(ref) * 2.0 ** -24).all()
+    y[1:M + 1, 3:N + 3] = -7
+    assert (y == -7).all()
+
+
+def test_gemm_for_a_batch_scales_at_odd_addresses():
+    """Scales and zero points that do not begin on a 16-byte boundary: the same values."""
+    rng = np.random.default_rng(14)
+    (wq, sg, zp), w = random_weight(rng, 528, 136, 64, True)
+    off_s = torch.empty(sg.numel() + 1, dtype=sg.dtype, device=DEV)[1:].view(sg.shape).copy_(sg)
+    off_z = torch.empty(zp.numel() + 1, dtype=zp.dtype, device=DEV)[1:].view(zp.shape).copy_(zp)
+    x = activations(rng, 40, 528, "bf16")
+    for s, z in ((sg, zp), (off_s, off_z)):
+        check(sq.sq_w4_gemm(dev(x, "bf16"), wq, s, z, group=64, out_dtype=torch.float32), *P.product(x, w, 64), "f32")
+
+
+def test_gemm_for_a_batch_two_streams_and_graphs():
+    rng = np.random.default_rng(15)
+    (wq, sg, zp), w = random_weight(rng, 2048, 1160, 64, True)
+    x = [activations(rng, m, 2048, "bf16") for m in (16, 64)]
+    xd = [dev(a, "bf16") for a in x]
+    want = [sq.sq_w4_gemm(a, wq, sg, zp, group=64) for a in xd]
+    for a, y in zip(x, want):
+        check(y, *P.product(a, w, 64), "bf16")
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    ys = [torch.empty_like(y) for y in want]
+    torch.cuda.synchronize()
+    for _ in range(40):
+        for a, st, y in zip(xd, streams, ys):
+            sq.sq_w4_gemm(a, wq, sg, zp, group=64, y=y, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, v) for y, v in zip(ys, want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for a, y in zip(xd, ys):
+            sq.sq_w4_gemm(a, wq, sg, zp, group=64, y=y)
+    for y in ys:
+        y.zero_()
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, v) for y, v in zip(ys, want))
+    assert sq.sq_device_error() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(16, 4096, 256), (64, 4096, 4096)])
+def test_gemm_for_a_batch_gives_up(M, N, K):
+    """Every wait runs out at once (one CTA a tile, then clusters): the kernel leaves and says so, and the next call is
+    right again."""
+    rng = np.random.default_rng(16)
+    (wq, sg, _), w = random_weight(rng, K, N, 128, False)
+    x = activations(rng, M, K, "bf16")
+    xd = dev(x, "bf16")
+    torch.cuda.synchronize()
+    sq.sq_device_error(clear=True)
+    sq.sq_set_wait_limit(0)
+    try:
+        sq.sq_w4_gemm(xd, wq, sg)
+        assert sq.sq_device_error(clear=True) & 7
+    finally:
+        torch.cuda.synchronize()
+        sq.sq_set_wait_limit(sq.WAIT_LIMIT_DEFAULT_NS)
+        sq.sq_device_error(clear=True)
+    check(sq.sq_w4_gemm(xd, wq, sg, out_dtype=torch.float32), *P.product(x, w, 128), "f32")
+    assert sq.sq_device_error(clear=True) == 0
+
+
 def test_gemm_many_tokens():
     rng = np.random.default_rng(6)
     (wq, sg, zp), w = random_weight(rng, 272, 100, 128, False)

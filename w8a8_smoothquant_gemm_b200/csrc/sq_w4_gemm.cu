@@ -210,6 +210,10 @@ __global__ void __launch_bounds__(32 * W4G_WARPS, 1) w4_gemm_kernel(const W4Gemm
 }  // namespace sqk
 
 namespace sqh {
+cudaError_t launch_w4_tc(const void* x, bool bf16, int64_t M, int64_t K, int64_t ldx, const uint8_t* wq,
+                         const uint16_t* sg, const uint8_t* zp, int64_t N, int group, void* y, bool y_bf16, int64_t ldy,
+                         bool* taken, cudaStream_t st);
+
 namespace {
 
 constexpr int64_t kSmemBudget = 226 * 1024;  // of 227 KB; the rest covers the static arrays
@@ -320,6 +324,14 @@ cudaError_t launch_w4_gemm_g(const sqk::W4GemmParams& p, int group, cudaStream_t
 cudaError_t launch_w4_gemm(const void* x, bool bf16, int64_t M, int64_t K, int64_t ldx, const uint8_t* wq,
                            const uint16_t* sg, const uint8_t* zp, int64_t N, int group, void* y, bool y_bf16,
                            int64_t ldy, cudaStream_t st) {
+  // More tokens than a column tile of 8: the kernel that unpacks a code once for up to 64 of them, if the
+  // scales come in 16-byte pieces and x fits (one to eight tokens: 16.6 against 26 us at 28672 x 4096, 20.8
+  // against 31 at 12288 x 12288; nine to sixteen 11.3 and 9.1 at 4096 x 4096, alike at the larger ones).
+  if (M > 8 && N % 8 == 0 && (uintptr_t)sg % 16 == 0 && (uintptr_t)zp % 8 == 0) {
+    bool taken = false;
+    const cudaError_t e = launch_w4_tc(x, bf16, M, K, ldx, wq, sg, zp, N, group, y, y_bf16, ldy, &taken, st);
+    if (e != cudaSuccess || taken) return e;
+  }
   sqk::W4GemmParams p{};
   p.x = (const char*)x;
   p.ldx_bytes = ldx * (bf16 ? 2 : 4);
@@ -335,9 +347,8 @@ cudaError_t launch_w4_gemm(const void* x, bool bf16, int64_t M, int64_t K, int64
   p.y = y;
   p.ldy = ldy;
   p.y_bf16 = y_bf16;
-  // up to 8 tokens fill a column tile; more take blocks of 16 (grid y), each reading the weights again,
-  // from L2: a CTA that held 32 or more tokens would have room for too few tiles' sums beside x (64 tokens,
-  // 4096 x 4096: 16 us against 19 to 39)
+  // up to 8 tokens fill a column tile; more (where the other kernel cannot take them) come in blocks of 16
+  // (grid y), each reading the weights again, from L2
   if (bf16) return M <= 8 ? launch_w4_gemm_g<1, 1>(p, group, st) : launch_w4_gemm_g<2, 1>(p, group, st);
   return M <= 8 ? launch_w4_gemm_g<1, 3>(p, group, st) : launch_w4_gemm_g<2, 3>(p, group, st);
 }
