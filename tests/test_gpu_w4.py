@@ -154,7 +154,7 @@ def test_gemm_sizes(M, K, N, group, asym, dt):
 @pytest.mark.parametrize("group,asym,dt", [(32, True, "bf16"), (64, False, "bf16"), (128, True, "bf16"), (128, False, "f32"),
                                            (64, True, "f32"), (32, False, "f32")])
 def test_gemm_many_channels_for_few_tokens(M, group, asym, dt):
-    """Enough tiles for the products in digits; tokens of very different magnitudes, one of them zero."""
+    """Many tiles to a CTA; tokens of very different magnitudes, one of them zero."""
     rng = np.random.default_rng(M + group)
     K, N = 528, 21008
     (wq, sg, zp), w = random_weight(rng, K, N, group, asym)

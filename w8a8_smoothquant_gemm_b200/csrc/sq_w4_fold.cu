@@ -16,6 +16,8 @@
 // the format) of 64 output channels; each thread two output channels and one 32-code word column,
 // so a group's extremes are in registers (group 32) or meet through shared memory once, and the two
 // channels' quotients run on packed binary32 pairs (one reciprocal a group, Markstein's correction).
+// Measured (4096 x 28672 bf16, group 64, zero points): 85 us, 3.5 TB/s, bound by issue; the values 52 us, 5.7 TB/s
+// of codes read and values written.
 #include <algorithm>
 
 #include "sq_w4.cuh"

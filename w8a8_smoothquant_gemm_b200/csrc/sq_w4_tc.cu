@@ -20,6 +20,14 @@
 //
 // A cluster of C CTAs cuts K, so that x fits; the CTAs' sums of a tile meet through distributed shared
 // memory (every rank adds, in the order of the ranks, a slice of the tokens).  Waits are bounded.
+//
+// Measured: 64 x 4096 x 4096 13.0 us (blocks of 16 tokens on mma.sync: 16.0), 64 x 28672 x 4096 39.7 (77),
+// 32 x 28672 x 4096 26.9 (42), 64 x 12288 x 12288 66 (106), 16 x 128256 x 4096 80 (86).  A block of 128 x 128
+// codes takes some 640 clocks of an SM at 16 tokens, of which the integer pipe needs 250 for the unpacking and
+// the matrix instructions 224: the rest is the chain of barriers between the roles.  A third unpacking
+// warpgroup and reading the next sums ahead of the additions changed nothing.  At 64 x 28672 x 4096: the exchange by
+// plain stores with cluster-wide fences, and a single lane in the issuing loop, 123 us; st.async and the whole
+// warp in the loop 61; a warpgroup of its own for what comes in 47; its code unrolled per cluster size 41.
 #include <algorithm>
 #include <type_traits>
 
@@ -149,6 +157,9 @@ __global__ void __launch_bounds__(tc_threads(TB), 1) w4_tc_kernel(const W4TcPara
   constexpr int GPB = 4 / GW, GPU = 2 * GPB;  // groups of a block, of a unit
   constexpr int DW = tc_adders(TB), TW = TB / DW, OUT_WARP = 4 * DW + 8, MMA_WARP = OUT_WARP + 4, THREADS = tc_threads(TB);
   constexpr int SLOT = tc_slot(GW, ASYM), SCALES = tc_scale_slot(GW);
+  // One group a block and as many accumulators as operand buffers: one commit says both that the sums are there
+  // and that the operands have been used.
+  constexpr bool ONE = GPB == 1 && ND == TC_A_BUFS;
   static_assert(NC % 16 == 0 && ND * NC + TC_A_BUFS * TC_A_COLS <= 512, "tensor memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -317,15 +328,21 @@ __global__ void __launch_bounds__(tc_threads(TB), 1) w4_tc_kernel(const W4TcPara
     for (int i = 0; ok && i < total; ++i) {
       for (int b = 0; ok && b < 2; ++b) {
         const int buf = 2 * (i & 1) + b;
-        ok = __all_sync(0xffffffffu, mbar_wait(a_full(buf), (i >> 1) & 1, limit));
+        // the operands and the first group's accumulator: looked at together, the answers take a while
+        const uint32_t a_par = (i >> 1) & 1;
+        const bool a_there = mbar_try_wait(a_full(buf), a_par), d_there = mbar_try_wait(d_empty(d), d_par);
+        ok = limit != 0 && (a_there || mbar_wait(a_full(buf), a_par, limit)) && (d_there || mbar_wait(d_empty(d), d_par, limit));
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         const uint32_t a = tmem + buf * TC_A_COLS;
         const uint64_t x = sw128_desc(sbase + (u * 4 + b * 2) * (NC * 128));
         for (int g = 0; g < GPB; ++g) {
-          ok = __all_sync(0xffffffffu, mbar_wait(d_empty(d), d_par, limit));
-          if (!ok) break;
-          tc_fence_after();
+          if (g > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(d_empty(d), d_par, limit));
+            if (!ok) break;
+            tc_fence_after();
+          }
 #pragma unroll
           for (int s = 0; s < 8 / GPB; ++s) {
             const int step = g * (8 / GPB) + s;
@@ -337,7 +354,7 @@ __global__ void __launch_bounds__(tc_threads(TB), 1) w4_tc_kernel(const W4TcPara
             d_par ^= 1;
           }
         }
-        tc_commit_if(on, a_empty(buf));
+        if (!ONE) tc_commit_if(on, a_empty(buf));
       }
       if (++u == (uint32_t)units) u = 0;
     }
@@ -439,7 +456,7 @@ __global__ void __launch_bounds__(tc_threads(TB), 1) w4_tc_kernel(const W4TcPara
             }
           }
           if (h == 0) {  // the buffer's last operands have been used
-            ok = __all_sync(0xffffffffu, mbar_wait(a_empty(2 * wg + b), par, limit));
+            ok = __all_sync(0xffffffffu, mbar_wait(ONE ? d_full(2 * wg + b) : a_empty(2 * wg + b), par, limit));
             if (!ok) break;
             tc_fence_after();
           }
@@ -620,7 +637,9 @@ cudaError_t launch_w4_tc_t(sqk::W4TcParams p, bool* taken, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   attr[1].val.clusterDim.x = (unsigned)p.C;
   cfg.gridDim = dim3((unsigned)(p.clusters * p.C), (unsigned)mt);
-  cfg.dynamicSmemBytes = (size_t)(1024 + p.bar_at + 8 * sqk::TC_BARS);
+  // All of an SM's shared memory, whatever is used of it: no other kernel that allocates tensor memory may share
+  // the SM, since two clusters that each held an SM the other waits for would never go on.
+  cfg.dynamicSmemBytes = (size_t)kSmemBudget;
   cfg.attrs = attr;
   cfg.numAttrs = p.C > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
