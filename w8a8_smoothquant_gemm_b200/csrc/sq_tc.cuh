@@ -1,5 +1,6 @@
 // sq_tc.cuh -- wrappers of the 5th-generation tensor cores' instructions (tcgen05) and of cluster-wide
-// barriers, shared by the GEMMs.
+// barriers for the batch kernel of the 4-bit product.  (sq_gemm.cu has its own: the traffic figure that
+// bench.py quotes is tied to that file's text.)
 #pragma once
 
 #include "sq_ptx.cuh"
@@ -20,12 +21,7 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-// Shared-memory matrix descriptor of a K-major tile with 128-byte
-// swizzle: rows of 128 bytes, 8-row swizzle atoms 1024 bytes apart (stride byte
+// Shared-memory matrix descriptor of a K-major tile with 128-byte swizzle: rows of 128 bytes, 8-row swizzle atoms 1024 bytes apart (stride byte
 // offset), leading byte offset unused for swizzled K-major layouts, descriptor version 1
 // (sm_100), layout code 2 = 128-byte swizzle.  The tile base is 1024-byte aligned; the
 // k-th 32-byte step inside a row advances the start address by 32 bytes.
