@@ -175,3 +175,18 @@ def test_binding_refuses_what_the_call_could_not_see():
         sq.sq_w4_dequant(wq, sg, K=256, group=48)
     with pytest.raises(ValueError):
         sq.sq_fold_quant_weights_w4(torch.zeros(256, 8, dtype=torch.bfloat16))
+
+
+def test_binding_refuses_a_stream_of_another_device():
+    import types
+    there = types.SimpleNamespace(device_index=0)
+    x = torch.zeros(2, 256, dtype=torch.bfloat16)  # not on device 0
+    wq, sg = torch.zeros(8, 128, dtype=torch.uint8), torch.zeros(2, 8, dtype=torch.bfloat16)
+    w13, s13 = torch.zeros(2, 32, 128, dtype=torch.uint8), torch.zeros(2, 2, 32, dtype=torch.bfloat16)
+    ids, wts = torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, 1)
+    for call in (lambda: sq.sq_w4_gemm(x, wq, sg, stream=there), lambda: sq.sq_w4_dequant(wq, sg, K=256, stream=there),
+                 lambda: sq.sq_fold_quant_weights_w4(x, stream=there),
+                 lambda: sq.sq_moe_w4(x, x, 1, w13, s13, w13, s13, stream=there),
+                 lambda: sq.sq_moe_w4_routed(x, ids, wts, w13, s13, w13, s13, stream=there)):
+        with pytest.raises(ValueError, match="another device"):
+            call()
