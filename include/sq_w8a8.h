@@ -349,9 +349,9 @@ sq_status sq_w4_dequant(const uint8_t* Wq, const uint16_t* scales, const uint8_t
  *   y[m, n] = sum over groups of scale * (sum over the group's k of (code[n, k] - zero) * x[m, k])
  *   x: [M, K] bf16 or fp32, ldx; both enter exactly (fp32 as a sum of three bf16 numbers), sums are
  *   binary32, and the result is rounded once to ydt (SQ_BF16 or SQ_F32).  y: [M, N], ldy >= N,
- *   aligned to its element size.  K % 16 == 0, K <= SQ_MAX_K.  Weights are read once for up to 64
- *   tokens (32 or 16 where K > 4096; 16 where N % 8 != 0 or scales or zeros do not begin on a 16-byte
- *   boundary); more tokens (up to SQ_W4_MAX_M) read them again, from L2 where they fit.  No
+ *   aligned to its element size.  K % 16 == 0, K <= SQ_MAX_K.  Weights are read once for up to 16
+ *   tokens, and where N and K are large enough for up to 64 (32 where K > 4096; not where N % 8 != 0
+ *   or scales or zeros do not begin on a 16-byte boundary, nor with bf16 x and groups of 32); more tokens (up to SQ_W4_MAX_M) read them again, from L2 where they fit.  No
  *   workspace; the order of the sums depends on the sizes and on that alignment alone, so equal
  *   calls give equal bits. */
 sq_status sq_w4_gemm(const void* x, sq_dtype dt, int64_t M, int64_t K, int64_t ldx, const uint8_t* Wq,

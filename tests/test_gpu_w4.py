@@ -171,7 +171,11 @@ def test_gemm_many_channels_for_few_tokens(M, group, asym, dt):
 @pytest.mark.parametrize("K,N,group,asym,dt", [(16, 8, 128, False, "bf16"), (128, 136, 32, True, "bf16"),
                                                (400, 128, 64, True, "bf16"), (1040, 1000, 64, False, "f32"),
                                                (2064, 4104, 128, True, "bf16"), (272, 40, 32, True, "f32"),
-                                               (4096, 520, 32, True, "bf16"), (8192, 264, 128, False, "f32")])
+                                               (4096, 520, 32, True, "bf16"), (8192, 264, 128, False, "f32"),
+                                               (4096, 1032, 64, True, "bf16"), (2064, 2056, 128, False, "bf16"),
+                                               (4096, 2056, 128, True, "bf16"), (144, 30008, 128, True, "bf16"),
+                                               (14336, 1096, 64, False, "bf16"), (4096, 1160, 128, True, "f32"),
+                                               (400, 10488, 64, False, "f32"), (4112, 4104, 32, True, "f32")])
 def test_gemm_for_a_batch(M, K, N, group, asym, dt):
     """Nine tokens and more, whole pieces of scales: last units of one block, last tiles of few channels, blocks of
     tokens that are not full, K over clusters."""
@@ -200,7 +204,7 @@ def test_gemm_for_a_batch_many_tiles(M, K, N, group, asym, dt):
 @pytest.mark.parametrize("M", [9, 20, 64])
 def test_gemm_for_a_batch_is_exact_on_integers(M):
     rng = np.random.default_rng(M)
-    K, N = 1296, 2056
+    K, N = 1296, 3240
     codes = rng.integers(0, 16, (N, K)).astype(np.uint8)
     sg = (2.0 ** rng.integers(-3, 4, (-(-K // 64), N))).astype(np.float32)
     zp = rng.integers(0, 16, sg.shape).astype(np.uint8)
@@ -213,9 +217,10 @@ def test_gemm_for_a_batch_is_exact_on_integers(M):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_gemm_for_a_batch_strides_infinities_and_the_rows_behind(dt):
+@pytest.mark.parametrize("N", [264, 10504])
+def test_gemm_for_a_batch_strides_infinities_and_the_rows_behind(dt, N):
     rng = np.random.default_rng(13)
-    M, K, N = 21, 400, 264
+    M, K = 21, 400
     codes = rng.integers(9, 16, (N, K)).astype(np.uint8)  # positive weights only
     sg = P.bf16(rng.uniform(0.5, 2, (4, N)).astype(np.float32))
     wq = P.pack(codes)
@@ -238,7 +243,7 @@ def test_gemm_for_a_batch_strides_infinities_and_the_rows_behind(dt):
 def test_gemm_for_a_batch_scales_at_odd_addresses():
     """Scales and zero points that do not begin on a 16-byte boundary: the same values."""
     rng = np.random.default_rng(14)
-    (wq, sg, zp), w = random_weight(rng, 528, 136, 64, True)
+    (wq, sg, zp), w = random_weight(rng, 528, 8008, 64, True)
     off_s = torch.empty(sg.numel() + 1, dtype=sg.dtype, device=DEV)[1:].view(sg.shape).copy_(sg)
     off_z = torch.empty(zp.numel() + 1, dtype=zp.dtype, device=DEV)[1:].view(zp.shape).copy_(zp)
     x = activations(rng, 40, 528, "bf16")
@@ -248,8 +253,8 @@ def test_gemm_for_a_batch_scales_at_odd_addresses():
 
 def test_gemm_for_a_batch_two_streams_and_graphs():
     rng = np.random.default_rng(15)
-    (wq, sg, zp), w = random_weight(rng, 2048, 1160, 64, True)
-    x = [activations(rng, m, 2048, "bf16") for m in (16, 64)]
+    (wq, sg, zp), w = random_weight(rng, 2048, 2056, 64, True)
+    x = [activations(rng, m, 2048, "bf16") for m in (24, 64)]
     xd = [dev(a, "bf16") for a in x]
     want = [sq.sq_w4_gemm(a, wq, sg, zp, group=64) for a in xd]
     for a, y in zip(x, want):
@@ -275,7 +280,7 @@ def test_gemm_for_a_batch_two_streams_and_graphs():
     assert sq.sq_device_error() == 0
 
 
-@pytest.mark.parametrize("M,N,K", [(16, 4096, 256), (64, 4096, 4096)])
+@pytest.mark.parametrize("M,N,K", [(32, 20000, 256), (64, 4096, 4096)])
 def test_gemm_for_a_batch_gives_up(M, N, K):
     """Every wait runs out at once (one CTA a tile, then clusters): the kernel leaves and says so, and the next call is
     right again."""

@@ -323,16 +323,31 @@ cudaError_t launch_w4_gemm_g(const sqk::W4GemmParams& p, int group, cudaStream_t
   return launch_w4_gemm_a<NT, S, 4, false>(p, st);
 }
 
+// Whether the kernel that unpacks a code once for a batch of tokens (sq_w4_tc.cu) is the faster one.  Its fixed
+// costs want 4 M codes and 8 tiles of 128 channels; this file's takes a block of 16 tokens at a time.  Measured, us,
+// this file's and that one:
+//   bf16, groups of 128, 32 tokens: 1024 x 4096 8.4 and 6.9, 4096 x 4096 13.0 and 9.4, 28672 x 4096 41.5 and 27.2
+//   (2048 x 768 4.8 and 6.3); 64 tokens: 4096 x 4096 16.5 and 13.3, 28672 x 4096 76 and 40
+//   16 tokens: 2048 x 4096 10.0 and 7.5, 4096 x 4096 11.3 and 8.3, 28672 x 4096 24.9 and 25.3 (9 tokens 22.8 and 25.1)
+//   binary32, 16 tokens: 2048 x 2048 9.5 and 7.1, 28672 x 4096 56 and 29; groups of 32 61 and 49 (2048 x 4096 11.2
+//   and 12.6)
+// Groups of 32 are four sums a block there, which the adding warps do not keep up with: bf16, 64 tokens, 4096 x 4096
+// 17.5 and 21.5; 16 tokens, 28672 x 4096 29 and 40.
+bool batch_kernel_pays(bool bf16, int64_t M, int64_t N, int64_t K, int group) {
+  const int64_t codes = N * K;
+  if (M <= 8 || N < 1024) return false;
+  if (!bf16) return codes >= (group == 32 ? 1 << 24 : 1 << 22);
+  if (group == 32) return false;
+  if (M <= 16) return group == 128 && N >= 2048 && codes >= 1 << 23 && codes <= 1 << 26;
+  return codes >= 1 << 22;
+}
+
 }  // namespace
 
 cudaError_t launch_w4_gemm(const void* x, bool bf16, int64_t M, int64_t K, int64_t ldx, const uint8_t* wq,
                            const uint16_t* sg, const uint8_t* zp, int64_t N, int group, void* y, bool y_bf16,
                            int64_t ldy, cudaStream_t st) {
-  // More tokens than a column tile of 8: the kernel that unpacks a code once for up to 64 of them, if the
-  // scales come in 16-byte pieces and x fits (1 to 8 tokens: this file's 17 to 19 us
-  // against 25 at 28672 x 4096, 21 to 24 against 30 at 12288 x 12288; 16 tokens: 11.3 against 8.2 at 4096 x 4096,
-  // 25.4 and 25.2, 33.4 against 30.7).
-  if (M > 8 && N % 8 == 0 && (uintptr_t)sg % 16 == 0 && (uintptr_t)zp % 8 == 0) {
+  if (batch_kernel_pays(bf16, M, N, K, group) && N % 8 == 0 && (uintptr_t)sg % 16 == 0 && (uintptr_t)zp % 8 == 0) {
     bool taken = false;
     const cudaError_t e = launch_w4_tc(x, bf16, M, K, ldx, wq, sg, zp, N, group, y, y_bf16, ldy, &taken, st);
     if (e != cudaSuccess || taken) return e;

@@ -647,12 +647,14 @@ cudaError_t launch_w4_tc_t(sqk::W4TcParams p, bool* taken, cudaStream_t st) {
 
 template <int TB, int S>
 cudaError_t launch_w4_tc_g(const sqk::W4TcParams& p, int group, bool* taken, cudaStream_t st) {
+  if constexpr (S > 1) {  // (groups of 32 come here with binary32 x alone)
+    if (group == 32)
+      return p.w.zeros ? launch_w4_tc_t<TB, S, 1, true>(p, taken, st) : launch_w4_tc_t<TB, S, 1, false>(p, taken, st);
+  }
   if (p.w.zeros) {
-    if (group == 32) return launch_w4_tc_t<TB, S, 1, true>(p, taken, st);
     if (group == 64) return launch_w4_tc_t<TB, S, 2, true>(p, taken, st);
     return launch_w4_tc_t<TB, S, 4, true>(p, taken, st);
   }
-  if (group == 32) return launch_w4_tc_t<TB, S, 1, false>(p, taken, st);
   if (group == 64) return launch_w4_tc_t<TB, S, 2, false>(p, taken, st);
   return launch_w4_tc_t<TB, S, 4, false>(p, taken, st);
 }
