@@ -3,7 +3,7 @@
 //
 // y[m, n] = sum_g scale[g, n] * sum_{k in g} (code[n, k] - zero[g, n]) * x[m, k]
 //
-// Beyond a column tile or two of mma.sync, what costs is no longer the weights' bytes but turning codes
+// Beyond two column tiles of mma.sync, what costs is no longer the weights' bytes but turning codes
 // into operands again for every 16 tokens.  Here a code is unpacked once for all tokens of a block:
 // the weights are the A operand (128 output channels), which tcgen05.mma takes from tensor memory, so
 // the unpacked pairs go from registers straight there (tcgen05.st, a thread per channel) and never
