@@ -1,0 +1,22 @@
+"""CPU: what the memory model asks of the 4-bit kernels and no run can show, read from their sources."""
+import glob
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "w8a8_smoothquant_gemm_b200", "csrc")
+
+
+def source(name):
+    """A file's code, without its comments."""
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def test_arrivals_on_other_blocks_barriers_release():
+    """An arrival at another block's barrier hands over memory that was read or written before it: only a release
+    orders that, a dependency between the values does not."""
+    names = [os.path.basename(p) for p in glob.glob(os.path.join(CSRC, "*.cu*"))]
+    arrivals = [(n, m) for n in names for m in re.findall(r"mbarrier\.arrive\S*shared::cluster\S*", source(n))]
+    assert any(n == "sq_tc.cuh" for n, _ in arrivals)
+    assert [a for a in arrivals if ".release.cluster." not in a[1]] == []
+    assert not [n for n in names if "relaxed" in source(n)]

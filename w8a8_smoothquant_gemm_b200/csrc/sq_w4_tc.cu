@@ -136,10 +136,6 @@ __device__ __forceinline__ void st_async4(uint32_t to, float2 a, float2 b, uint3
       : "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
 __device__ __forceinline__ void store_as(float* y, float v) { *y = v; }
 __device__ __forceinline__ void store_as(__nv_bfloat16* y, float v) { *y = __float2bfloat16_rn(v); }
 
@@ -373,7 +369,6 @@ __global__ void __launch_bounds__(tc_threads(TB), 1) w4_tc_kernel(const W4TcPara
         ok = __all_sync(0xffffffffu, mbar_wait_cluster(recv_full(par, q), (tile >> 1) & 1, limit));
         if (!ok) break;
         float4 v[FOURS];  // this rank's tokens, by fours
-        uint32_t seen = 0;
 #pragma unroll
         for (int k = 0; k < FOURS; ++k) {
           const float* from = recv + par * PARITY + (4 * k / SL) * (TW * TC_ROWS) + (4 * k % SL) * TC_ROWS + (q * 32 + lane) * 4;
@@ -384,13 +379,11 @@ __global__ void __launch_bounds__(tc_threads(TB), 1) w4_tc_kernel(const W4TcPara
 #pragma unroll
           for (int c = 1; c < C; ++c)
             v[k] = make_float4(__fadd_rn(v[k].x, o[c].x), __fadd_rn(v[k].y, o[c].y), __fadd_rn(v[k].z, o[c].z), __fadd_rn(v[k].w, o[c].w));
-          seen |= __float_as_uint(v[k].x);
         }
-        // The arrival hangs on what every lane has read (a zero that the compiler cannot know), so it needs
-        // no release, which would wait for the last tile's stores.
-        asm volatile("and.b32 %0, %0, 0;" : "+r"(seen));
-        seen = __reduce_or_sync(0xffffffffu, seen);
-        if (lane < C) mbar_arrive_cluster_relaxed(map_shared(recv_free(par, q), lane) + seen);
+        // Every lane has read: the arrivals release that to the ranks, which write here again after they have acquired
+        // it.  They come before this tile's stores, so all that they can wait for is the last tile's.
+        __syncwarp();
+        if (lane < C) mbar_arrive_cluster(map_shared(recv_free(par, q), lane));
         const int64_t n = (int64_t)(t_first + tile) * TC_ROWS + q * 32 + lane;
         if (n < p.N) {
           auto put = [&](auto* y) {
