@@ -20,3 +20,13 @@ def test_arrivals_on_other_blocks_barriers_release():
     assert any(n == "sq_tc.cuh" for n, _ in arrivals)
     assert [a for a in arrivals if ".release.cluster." not in a[1]] == []
     assert not [n for n in names if "relaxed" in source(n)]
+
+
+def test_a_block_stays_for_sums_under_way_after_the_last_cluster_barrier():
+    """When a wait has run out, sums that other blocks sent may still be coming.  The cluster barrier before the end says
+    that all are sent, not that they are there: the time that they are given has to follow it."""
+    text = source("sq_w4_tc.cu")
+    kernel = text[text.index("w4_tc_kernel(const W4TcParams p)"):]
+    kernel = kernel[:kernel.index("namespace sqh")]
+    assert kernel.count("__nanosleep") == 1
+    assert kernel.rindex("cluster_sync();") < kernel.index("__nanosleep")

@@ -315,6 +315,7 @@ __global__ void __launch_bounds__(tc_threads(TB), 1) w4_tc_kernel(const W4TcPara
   float* recv = reinterpret_cast<float*>(smem + p.recv_at);
   constexpr int PARITY = TB * TC_ROWS;
 
+  bool landed = true;  // all that other ranks send to this thread's part of the exchange buffer
   if (warp == MMA_WARP) {
     // ------------------------------------------------------------------ matrix instructions
     constexpr uint32_t IDESC = idesc_bf16(TC_ROWS, NC);
@@ -408,10 +409,7 @@ __global__ void __launch_bounds__(tc_threads(TB), 1) w4_tc_kernel(const W4TcPara
       if (p.C == 8) out(std::integral_constant<int, 8>{});
     }
     if (!ok && lane == 0) atomicOr(p.err, ERR_GEMM_EPILOGUE_WAIT);
-    if (!ok && p.C > 1) {  // what other ranks have sent lands before this CTA can leave
-      const unsigned long long t0 = global_ns();
-      for (uint32_t i = 0; i < (1u << 20) && global_ns() - t0 < 1000000ull; ++i) __nanosleep(1000);
-    }
+    landed = ok || p.C == 1;
   } else if (warp >= 4 * DW) {
     // ------------------------------------------------------------------ codes to operands
     const uint32_t tm = tmem + ((uint32_t)(q * 32) << 16) + 2 * wg * TC_A_COLS;
@@ -555,6 +553,12 @@ __global__ void __launch_bounds__(tc_threads(TB), 1) w4_tc_kernel(const W4TcPara
     __syncwarp();
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+  if (!landed) {
+    // A wait ran out, and sums that the others sent may still be on their way.  All were sent before the barrier
+    // above, which does not wait for them: this CTA's memory stays until they have come.
+    const unsigned long long t0 = global_ns();
+    for (uint32_t i = 0; i < (1u << 20) && global_ns() - t0 < 1000000ull; ++i) __nanosleep(1000);
   }
 }
 
