@@ -30,3 +30,12 @@ def test_a_block_stays_for_sums_under_way_after_the_last_cluster_barrier():
     kernel = kernel[:kernel.index("namespace sqh")]
     assert kernel.count("__nanosleep") == 1
     assert kernel.rindex("cluster_sync();") < kernel.index("__nanosleep")
+
+
+def test_blocks_without_tiles_wait_for_their_copies():
+    """A block of the gate/up kernel starts to copy the tokens before it knows whether it has a tile.  Without one it
+    never comes to the wait inside the loop over its tiles, and must not leave with copies to its memory under way."""
+    text = source("sq_moe.cu")
+    kernel = text[text.index("moe_up_kernel(const MoeParams p)"):text.index("moe_down_kernel(const MoeParams p)")]
+    assert kernel.index("moe_stage_rows(") < kernel.index("for (int p0 = 0;")
+    assert kernel.rindex("p.h[") < kernel.rindex("cp_wait_all();")

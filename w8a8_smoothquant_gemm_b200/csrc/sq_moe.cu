@@ -544,6 +544,7 @@ __global__ void __launch_bounds__(MOE_EXPERT_THREADS, 1) moe_up_kernel(const Moe
       for (int s = 0; s < SH; ++s) p.h[((int64_t)s * p.T * p.top_k + s0 + m) * p.F + ff] = (uint16_t)part[s];
     }
   }
+  cp_wait_all();  // a block without tiles has not waited for x
 }
 
 // Down: a tile is 16 rows d; its units are those of every entry in turn (a rank of a cluster takes
