@@ -329,7 +329,8 @@ int64_t sq_w4_row_bytes(int64_t K);
  *   zeros == NULL: scale = bf16(max|W'| * RN(1/7)), code = 8 + clamp(rne(W' / scale), -7, 7)
  *   zeros != NULL: lo = min(0, min W'), hi = max(0, max W'), scale = bf16((hi - lo) * RN(1/15)),
  *                  zero = clamp(rne(-lo / scale), 0, 15), code = clamp(rne(W' / scale) + zero, 0, 15)
- *   over the group's channels j; a zero scale gives the code 8 (zeros == NULL) or zero point and
+ *   over the group's channels j; RN(1/7) and RN(1/15) are binary32 constants (the product is within
+ *   2^-23 of the quotient).  A zero scale gives the code 8 (zeros == NULL) or zero point and
  *   code 0.  Wq: [N, sq_w4_row_bytes(K)] bytes, 16-byte aligned.  W must be finite.  K % 16 == 0,
  *   K <= SQ_MAX_K.  gamma_f, beta_f as for sq_fold_quant_weights (with s NULL: copies). */
 sq_status sq_fold_quant_weights_w4(const void* W, sq_dtype dt, int64_t K, int64_t N, int64_t ldw, const float* s,
@@ -350,10 +351,12 @@ sq_status sq_w4_dequant(const uint8_t* Wq, const uint16_t* scales, const uint8_t
  *   x: [M, K] bf16 or fp32, ldx; both enter exactly (fp32 as a sum of three bf16 numbers), sums are
  *   binary32, and the result is rounded once to ydt (SQ_BF16 or SQ_F32).  y: [M, N], ldy >= N,
  *   aligned to its element size.  K % 16 == 0, K <= SQ_MAX_K.  Weights are read once for up to 16
- *   tokens, and where N and K are large enough for up to 64 (32 where K > 4096; not where N % 8 != 0
- *   or scales or zeros do not begin on a 16-byte boundary, nor with bf16 x and groups of 32); more tokens (up to SQ_W4_MAX_M) read them again, from L2 where they fit.  No
- *   workspace; the order of the sums depends on the sizes and on that alignment alone, so equal
- *   calls give equal bits. */
+ *   tokens.  Larger batches read them once for more where N >= 1024, N K >= 2^22 (2^24 with fp32 x
+ *   and groups of 32; never with bf16 x and groups of 32), N % 8 == 0, and scales begin on a
+ *   16-byte and zeros on an 8-byte boundary: bf16 x once for 64 tokens up to K = 4096, 32 up to
+ *   14336, fp32 x once for 32 up to 4096.  More tokens (up to SQ_W4_MAX_M) read them again, from
+ *   L2 where they fit.  No workspace; the order of the sums depends on the sizes and on that
+ *   alignment alone, so equal calls give equal bits. */
 sq_status sq_w4_gemm(const void* x, sq_dtype dt, int64_t M, int64_t K, int64_t ldx, const uint8_t* Wq,
                      const uint16_t* scales, const uint8_t* zeros, int64_t N, int group, void* y, sq_dtype ydt,
                      int64_t ldy, void* stream);

@@ -108,10 +108,11 @@ __device__ __forceinline__ void split_bf16_stored(float x, uint32_t part[S]) {
 //   What sets the depth is latency: at 6.5 TB/s and about 1 us under load an SM needs some 45 KB in
 // flight; 16 warps with a unit each on its way and one at work have 32 to 64 KB, and asking the L2 for
 // 256 bytes where the copies take 128 of a row fetches what the warp wants next (231 MB of weights: 47.8
-// us with the hint, 55.7 without; DEPTH 3 is 3 % faster there and 10 % slower at 30 MB).  What limits the
-// loop once the bytes are there is the unpacking (56 shifts and logic operations a block on the half-rate integer pipe,
-// about 29 clocks of an SM, against 46 in which HBM delivers a block), so everything else in it is
-// kept few: two blocks to a unit halve the control and address arithmetic.
+// us with the hint, 55.7 without; DEPTH 3 is 3 % faster there and 10 % slower at 30 MB).  Once the bytes are
+// there a block takes 58 to 61 clocks of an SM, against 46 in which HBM delivers it, with no unit at its limit:
+// the unpacking (56 shifts and logic operations a block on the half-rate integer pipe) fills 28 of them, its 143
+// instructions 36, the tensor pipe about 16; a scheduler's four warps lose the rest to a full math pipe, to each other
+// and to loads.  So everything else in the loop is kept few: two blocks to a unit halve the control and address arithmetic.
 constexpr int W4_UNIT = 2 * W4_BLOCK;
 
 __host__ __device__ __forceinline__ int w4_units(int64_t K) { return (int)((K + W4_UNIT - 1) / W4_UNIT); }
@@ -324,7 +325,9 @@ struct W4Runs {  // in shared memory
   int first_cell[WARPS], first_tile[WARPS], cells;
 };
 
-// n / d for n < 2^27 with inv = 1 / d: the quotient in binary32 is off by less than one.
+// n / d for n >= 0 and a quotient below 2^22, with inv = 1 / d: (float)n, inv and the product are each off by at
+// most 2^-24 of themselves, so the product by less than one, and its integer part by one at most.  (Quotients
+// here are tokens, rows, tiles or runs: thousands.)
 __device__ __forceinline__ int w4_div(int n, int d, float inv) {
   const int q = (int)__fmul_rn((float)n, inv), r = n - q * d;
   return q + (r >= d) - (r < 0);

@@ -19,7 +19,7 @@
 //
 // Measured (bf16 x, group 128): 1 x 6144 x 4096 6.4 us, 1 x 4096 x 14336 11.1, 8 x 28672 x 4096 19.0,
 // 1 x 128256 x 4096 59 us = 4.7 TB/s of codes and scales; 7 x 12288 x 12288, group 64 with zero points, 26.5.
-// A block of 16 x 128 codes takes 58 to 61 clocks of an SM, against 46 in which HBM delivers it.
+// A block of 16 x 128 codes takes 58 to 61 clocks of an SM, against 46 in which HBM delivers it (sq_w4.cuh has why).
 #include <algorithm>
 
 #include "sq_w4.cuh"
@@ -329,8 +329,14 @@ cudaError_t launch_w4_gemm_g(const sqk::W4GemmParams& p, int group, cudaStream_t
 //   bf16, groups of 128, 32 tokens: 1024 x 4096 8.4 and 6.9, 4096 x 4096 13.0 and 9.4, 28672 x 4096 41.5 and 27.2
 //   (2048 x 768 4.8 and 6.3); 64 tokens: 4096 x 4096 16.5 and 13.3, 28672 x 4096 76 and 40
 //   16 tokens: 2048 x 4096 10.0 and 7.5, 4096 x 4096 11.3 and 8.3, 28672 x 4096 24.9 and 25.3 (9 tokens 22.8 and 25.1)
+//   (16384 x 4096 17.9 and 17.3, 24576 x 4096 23.1 and 23.0, 12288 x 12288 32.2 and 31.4; at 9 tokens 2048 x 4096 7.3
+//   and 7.9, 4096 x 4096 9.8 and 8.7, 16384 x 4096 16.6 and 16.1, 24576 x 4096 21.1 and 22.3)
+//   groups of 64, 9 / 16 / 32 tokens: 4096 x 4096 10.0 / 12.0 / 13.4 and 9.2 / 9.4 / 10.5, 6144 x 4096 11.7 / 12.7 / 16.2 and
+//   12.2 / 12.8 / 14.1, 16384 x 4096 16.6 / 18.7 / 27.3 and 18.1 / 19.4 / 22.0, 28672 x 4096 24.0 / 26.1 / 47.5 and
+//   29.3 / 29.4 / 33.0: up to 16 tokens the larger weights decide
 //   binary32, 16 tokens: 2048 x 2048 9.5 and 7.1, 28672 x 4096 56 and 29; groups of 32 61 and 49 (2048 x 4096 11.2
-//   and 12.6)
+//   and 12.6); 9 tokens: 2048 x 2048 8.6 and 7.2, 28672 x 4096 42 and 28, groups of 32 46 and 49
+//   N = 512, 8192 channels, bf16, 16 / 32 / 64 tokens: 6.7 / 8.8 / 10.0 and 11.1 / 8.9 / 9.2
 // Groups of 32 are four sums a block there, which the adding warps do not keep up with: bf16, 64 tokens, 4096 x 4096
 // 17.5 and 21.5; 16 tokens, 28672 x 4096 29 and 40.
 bool batch_kernel_pays(bool bf16, int64_t M, int64_t N, int64_t K, int group) {
@@ -367,8 +373,8 @@ cudaError_t launch_w4_gemm(const void* x, bool bf16, int64_t M, int64_t K, int64
   p.y = y;
   p.ldy = ldy;
   p.y_bf16 = y_bf16;
-  // up to 8 tokens fill a column tile; more (where the other kernel cannot take them) come in blocks of 16
-  // (grid y), each reading the weights again, from L2
+  // up to 8 tokens fill a column tile; more (where the other kernel does not pay, or does not fit) come in blocks of
+  // 16 (grid y), each reading the weights again, from L2
   if (bf16) return M <= 8 ? launch_w4_gemm_g<1, 1>(p, group, st) : launch_w4_gemm_g<2, 1>(p, group, st);
   return M <= 8 ? launch_w4_gemm_g<1, 3>(p, group, st) : launch_w4_gemm_g<2, 3>(p, group, st);
 }

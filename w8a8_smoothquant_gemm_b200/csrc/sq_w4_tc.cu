@@ -21,8 +21,8 @@
 // A cluster of C CTAs cuts K, so that x fits; the CTAs' sums of a tile meet through distributed shared
 // memory (every rank adds, in the order of the ranks, a slice of the tokens).  Waits are bounded.
 //
-// Measured: 64 x 4096 x 4096 13.0 us (blocks of 16 tokens on mma.sync: 16.0), 64 x 28672 x 4096 39.7 (77),
-// 32 x 28672 x 4096 26.9 (42), 64 x 12288 x 12288 66 (106), 16 x 128256 x 4096 80 (86).  A block of 128 x 128
+// Measured: 64 x 4096 x 4096 13.3 us (blocks of 16 tokens on mma.sync: 16.4), 64 x 28672 x 4096 40.0 (77),
+// 32 x 28672 x 4096 26.9 (42), 64 x 12288 x 12288 65.3 (105).  A block of 128 x 128
 // codes takes some 640 clocks of an SM at 16 tokens, of which the integer pipe needs 250 for the unpacking and
 // the matrix instructions 224: the rest is the chain of barriers between the roles.  A third unpacking
 // warpgroup and reading the next sums ahead of the additions changed nothing.  At 64 x 28672 x 4096: the exchange by
